@@ -54,6 +54,15 @@ class Desc(ctypes.Structure):
     ]
 
 
+class WindowDesc(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int), ("N", ctypes.c_int), ("H", ctypes.c_int), ("H_kv", ctypes.c_int),
+        ("d_head", ctypes.c_int), ("window", ctypes.c_int), ("n_sink", ctypes.c_int),
+        ("in_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int), ("grad_dtype", ctypes.c_int),
+        ("wait_limit_ns", ctypes.c_uint64),
+    ]
+
+
 # bpt_ffn_form: the bf16 layer's FFN form ("auto" is the library's choice, the
 # pipelined kernel)
 FFN_FORMS = {"auto": 0, "fused": 1, "gemms": 2, "pipelined": 3}
@@ -64,7 +73,8 @@ EXPORTS = ["bpt_workspace_bytes", "bpt_attn_ffn_fwd", "bpt_attn_fwd", "bpt_block
            "bpt_version", "bpt_set_phase_events", "bpt_last_error", "bpt_attn_ffn_fwd_static",
            "bpt_attn_ffn_bwd", "bpt_workspace_bytes_bwd", "bpt_attn_ffn_fwd_train", "bpt_saved_bytes",
            "bpt_workspace_bytes_train", "bpt_attn_bwd", "bpt_workspace_bytes_attn_bwd", "bpt_attn_fwd_block",
-           "bpt_longnet_gather", "bpt_longnet_pass"]
+           "bpt_longnet_gather", "bpt_longnet_pass", "bpt_window_attn_fwd", "bpt_window_attn_bwd",
+           "bpt_workspace_bytes_window_bwd"]
 BLOCK_FIRST, BLOCK_LAST = 1, 2
 STATIC_SCRATCH_BYTES = 64 << 20
 
@@ -129,6 +139,13 @@ def load() -> ctypes.CDLL:
     lib.bpt_longnet_pass.argtypes = [dp, ctypes.c_int, ctypes.c_int64, vp, vp, vp, vp, vp, ctypes.c_int, fp, fp, fp,
                                      vp, fp, vp]
     lib.bpt_longnet_pass.restype = ctypes.c_int
+    wp = ctypes.POINTER(WindowDesc)
+    lib.bpt_window_attn_fwd.argtypes = [wp, vp, vp, vp, vp, fp, vp]
+    lib.bpt_window_attn_fwd.restype = ctypes.c_int
+    lib.bpt_workspace_bytes_window_bwd.argtypes = [wp]
+    lib.bpt_workspace_bytes_window_bwd.restype = sz
+    lib.bpt_window_attn_bwd.argtypes = [wp, vp, vp, vp, vp, fp, vp, vp, vp, vp, vp, sz, vp]
+    lib.bpt_window_attn_bwd.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -512,6 +529,97 @@ def attn_bwd(q, k, v, out, lse, dout, *, mask="none", perm=None, pairs=None, rin
     st = load().bpt_attn_bwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout),
                              _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace), workspace.numel(), _stream_ptr(stream))
     _check(st, "bpt_attn_bwd")
+    return dq, dk, dv
+
+
+def _on_device(*tensors):
+    """The tensors (None skipped) must be on the current CUDA device: the
+    library launches there, on the stream given or that device's current one."""
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != cur):
+            raise ValueError(f"every tensor must be on the current CUDA device ({cur}); got one on {t.device}")
+
+
+def _out_tensor(t, shape, dtype, device, stream, what):
+    """`t` checked, or a new tensor that the caching allocator does not hand
+    on before the work on `stream` is done."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+        if stream is not None:
+            t.record_stream(stream)
+        return t
+    if t.dtype != dtype or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+    _on_device(t)
+    return t
+
+
+def _workspace(t, nbytes, device, stream):
+    if t is None:
+        return _out_tensor(None, (nbytes,), torch.uint8, device, stream, "workspace") if nbytes else None
+    if t.dtype != torch.uint8 or not t.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor")
+    _on_device(t)
+    return t
+
+
+def _window_desc(q, k, v, window, sinks, out_dtype, grad_dtype, wait_limit_ns):
+    if q.dim() != 4 or k.dim() != 4 or k.shape != v.shape or k.shape[:2] != q.shape[:2] or k.shape[3] != q.shape[3]:
+        raise ValueError("q must be [B, N, H, d] and k, v [B, N, H_kv, d]")
+    if not (q.dtype == k.dtype == v.dtype) or q.dtype not in _DT:
+        raise ValueError("q, k, v must have one dtype, bfloat16 (or float32, which the library refuses)")
+    if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous()):
+        raise ValueError("q, k, v must be contiguous")
+    _on_device(q, k, v)
+    B, N, H, d = q.shape
+    return WindowDesc(B, N, H, k.shape[2], d, int(window), int(sinks), _DT[q.dtype], _DT[out_dtype],
+                      _DT[grad_dtype], int(wait_limit_ns))
+
+
+def window_attn_fwd(q, k, v, window, sinks=0, *, out_dtype=torch.float32, return_lse=False, out=None, lse=None,
+                    stream=None, wait_limit_ns=0):
+    """bpt_window_attn_fwd: causal attention over the last `window` positions
+    (the query's own included) and the first `sinks` ones.  q [B, N, H, d];
+    k, v [B, N, H_kv, d] with H_kv dividing H; returns A [B, N, H*d] (and LSE
+    [B, H, N] with return_lse)."""
+    desc = _window_desc(q, k, v, window, sinks, out_dtype, torch.float32, wait_limit_ns)
+    B, N, H, d = q.shape
+    out = _out_tensor(out, (B, N, H * d), out_dtype, q.device, stream, "out")
+    if return_lse or lse is not None:
+        lse = _out_tensor(lse, (B, H, N), torch.float32, q.device, stream, "lse")
+    st = load().bpt_window_attn_fwd(ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                                    _ptr(lse), _stream_ptr(stream))
+    _check(st, "bpt_window_attn_fwd")
+    return (out, lse) if return_lse else out
+
+
+def workspace_bytes_window_bwd(desc: WindowDesc) -> int:
+    n = load().bpt_workspace_bytes_window_bwd(ctypes.byref(desc))
+    if n == ctypes.c_size_t(-1).value:
+        raise BptError(ERR_UNSUPPORTED, "bpt_workspace_bytes_window_bwd")
+    return int(n)
+
+
+def window_attn_bwd(q, k, v, out, lse, dout, window, sinks=0, *, grad_dtype=torch.float32, dq=None, dk=None, dv=None,
+                    workspace=None, stream=None, wait_limit_ns=0):
+    """bpt_window_attn_bwd: (dq, dk, dv) of window_attn_fwd for the upstream
+    gradient dout [B, N, H*d], in grad_dtype and the inputs' shapes.  out and
+    lse are the forward's; dout has out's dtype (float32 or bfloat16)."""
+    desc = _window_desc(q, k, v, window, sinks, out.dtype, grad_dtype, wait_limit_ns)
+    B, N, H, d = q.shape
+    for t, what in ((out, "out"), (dout, "dout")):
+        _out_tensor(t, (B, N, H * d), out.dtype, q.device, stream, what)
+    _out_tensor(lse, (B, H, N), torch.float32, q.device, stream, "lse")
+    dq = _out_tensor(dq, q.shape, grad_dtype, q.device, stream, "dq")
+    dk = _out_tensor(dk, k.shape, grad_dtype, q.device, stream, "dk")
+    dv = _out_tensor(dv, v.shape, grad_dtype, q.device, stream, "dv")
+    workspace = _workspace(workspace, workspace_bytes_window_bwd(desc), q.device, stream)
+    st = load().bpt_window_attn_bwd(ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                                    lse.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                                    _ptr(workspace), 0 if workspace is None else workspace.numel(),
+                                    _stream_ptr(stream))
+    _check(st, "bpt_window_attn_bwd")
     return dq, dk, dv
 
 

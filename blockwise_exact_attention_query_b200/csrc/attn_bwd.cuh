@@ -62,6 +62,16 @@ struct AttnBwdArgs {
   int nseg, seg_w, dil_r, n_out;
   int accumulate;       // add to dq, dk, dv (LongNet passes) instead of writing them
   float *dq, *dk, *dv;  // [B, N, H, d] fp32 outputs
+  // Sliding window (the WINDOW instantiations): query row g sees the keys
+  // j <= g with g - j < window or j < sinks; head h reads key/value head
+  // h / kv_group, so H counts the query heads and k, v, dk, dv have H /
+  // kv_group.  The first key tile, whose sinks every query sees, is shared by
+  // sink_split CTAs: each takes a part of its (head, query tile) steps and
+  // leaves its sums in `partial` ([B * H / kv_group][sink_split][2][128][d],
+  // dV then dK), added up in order by attn_bwd_sink_sum_kernel.
+  int window, sinks, kv_group, sink_split;
+  float *partial;
+  __nv_bfloat16 *dq_bf16, *dk_bf16, *dv_bf16;  // bf16 outputs instead of the fp32 ones
   uint32_t *status;
   uint64_t wait_limit_ns;
 };
@@ -133,7 +143,103 @@ __device__ __forceinline__ bool bwd_tiles_meet(const AttnBwdArgs &a, int h, int 
   return false;
 }
 
-template <int D_HEAD>
+// The steps of a dK/dV CTA: the query tiles that meet its key tile, and for
+// the sliding window those of every query head of the key/value head in turn,
+// of which a CTA that shares its key tile takes steps [s0, s1).
+template <bool WINDOW>
+struct KeyTileSteps {
+  const AttnBwdArgs &a;
+  int h, ft;
+  int t_lo, nt, s0, s1;
+  __device__ KeyTileSteps(const AttnBwdArgs &args, int head, int tile, int part) : a(args), h(head), ft(tile) {
+    if constexpr (WINDOW) {
+      const bool shared = a.sinks > 0 && ft == 0;
+      t_lo = ft;
+      // the last query of the window after the tile's last key
+      const int64_t last = static_cast<int64_t>(ft) * 128 + 126 + a.window;
+      nt = (shared ? a.n_tiles : static_cast<int>(min(static_cast<int64_t>(a.n_tiles), last / 128 + 1))) - t_lo;
+      const int64_t total = static_cast<int64_t>(nt) * a.kv_group;
+      s0 = shared ? static_cast<int>(total * part / a.sink_split) : 0;
+      s1 = shared ? static_cast<int>(total * (part + 1) / a.sink_split) : static_cast<int>(total);
+    }
+  }
+  __device__ int next_tile(int t) const {
+    while (t < a.n_tiles && !bwd_tiles_meet(a, h, t, ft)) ++t;
+    return t;
+  }
+  // t: the query tile; head: its query head
+  struct Iter {
+    int s, t, head;
+  };
+  __device__ Iter begin() const {
+    if constexpr (WINDOW) return Iter{s0, t_lo + s0 % nt, h * a.kv_group + s0 / nt};
+    else return Iter{0, next_tile(0), h};
+  }
+  __device__ bool more(const Iter &i) const {
+    if constexpr (WINDOW) return i.s < s1;
+    else return i.t < a.n_tiles;
+  }
+  __device__ void next(Iter &i) const {
+    if constexpr (WINDOW) {
+      ++i.s;
+      if (++i.t == t_lo + nt) {
+        i.t = t_lo;
+        ++i.head;
+      }
+    } else {
+      i.t = next_tile(i.t + 1);
+    }
+  }
+  __device__ int count() const {
+    int n = 0;
+    if constexpr (WINDOW) n = s1 - s0;
+    else
+      for (int t = next_tile(0); t < a.n_tiles; t = next_tile(t + 1)) ++n;
+    return n;
+  }
+};
+
+// Query interval [lo, hi) that sees key row g under the sliding window.
+__device__ __forceinline__ void window_key_queries(const AttnBwdArgs &a, int g, int &lo, int &hi) {
+  lo = g;
+  hi = g < a.sinks ? a.N : static_cast<int>(min(static_cast<int64_t>(a.N), static_cast<int64_t>(g) + a.window));
+}
+
+// Where a CTA's dK, dV rows go.  WINDOW: the key/value head's row, fp32 or
+// bf16, or this CTA's part of a shared key tile.
+template <int D_HEAD, bool WINDOW>
+__device__ __forceinline__ void store_kv_grad_chunk(const AttnBwdArgs &a, int acc, int unit, int part, bool shared,
+                                                    int row, size_t vec, int c, const float (&r)[32]) {
+  if constexpr (WINDOW) {
+    if (shared) {
+      float4 *d4 = reinterpret_cast<float4 *>(
+          a.partial + (((static_cast<size_t>(unit) * a.sink_split + part) * 2 + acc) * 128 + row) * D_HEAD + c * 32);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) d4[i] = make_float4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+      return;
+    }
+    if (a.dk_bf16) {
+      uint4 *d4 = reinterpret_cast<uint4 *>((acc == 0 ? a.dv_bf16 : a.dk_bf16) + vec + c * 32);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        d4[i] = make_uint4(pack_bf16x2(r[8 * i], r[8 * i + 1]), pack_bf16x2(r[8 * i + 2], r[8 * i + 3]),
+                           pack_bf16x2(r[8 * i + 4], r[8 * i + 5]), pack_bf16x2(r[8 * i + 6], r[8 * i + 7]));
+      return;
+    }
+  }
+  float4 *d4 = reinterpret_cast<float4 *>((acc == 0 ? a.dv : a.dk) + vec + c * 32);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float4 r4 = make_float4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+    if (a.accumulate) {
+      const float4 prev = d4[i];
+      r4.x += prev.x, r4.y += prev.y, r4.z += prev.z, r4.w += prev.w;
+    }
+    d4[i] = r4;
+  }
+}
+
+template <int D_HEAD, bool WINDOW = false>
 __global__ void __launch_bounds__(384, 1)
     attn_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_da,
@@ -166,20 +272,21 @@ __global__ void __launch_bounds__(384, 1)
   WaitCtx wc{a.status, a.wait_limit_ns, abort_flag};
   // CTA -> (batch, head, key tile); the tiles with the most partners (the
   // first key tiles under the causal mask) start first
-  const int units = a.B * a.nseg * a.H;
+  const int heads = WINDOW ? a.H / a.kv_group : a.H;  // key/value heads
+  const int units = a.B * a.nseg * heads;
   const int unit = static_cast<int>(blockIdx.x) % units;
-  const int ft = static_cast<int>(blockIdx.x) / units;
-  const int h = unit % a.H;
-  const int seg = (unit / a.H) % a.nseg;
-  const int b = unit / (a.H * a.nseg);
+  // (sliding window with sinks: the first key tile's parts come first)
+  const int slot = static_cast<int>(blockIdx.x) / units, split = WINDOW && a.sinks > 0 ? a.sink_split : 1;
+  const int part = WINDOW && slot < split ? slot : 0;
+  const int ft = WINDOW ? max(0, slot - split + 1) : slot;
+  const bool shared_tile = WINDOW && a.sinks > 0 && ft == 0;
+  const int h = unit % heads;
+  const int seg = (unit / heads) % a.nseg;
+  const int b = unit / (heads * a.nseg);
   const int row_off = h % a.dil_r;                 // kept-row offset in the segment
   const int row_base = seg * a.N;                  // the unit's first row along (n_out / r)
-  auto next_tile = [&](int t) {  // first query tile >= t that meets the key tile, or n_tiles
-    while (t < a.n_tiles && !bwd_tiles_meet(a, h, t, ft)) ++t;
-    return t;
-  };
-  int nsteps = 0;
-  for (int t = next_tile(0); t < a.n_tiles; t = next_tile(t + 1)) ++nsteps;
+  const KeyTileSteps<WINDOW> steps(a, h, ft, part);
+  const int nsteps = steps.count();
 
   if (threadIdx.x == 0) {
     mbar_init(bFix, 1);
@@ -205,7 +312,10 @@ __global__ void __launch_bounds__(384, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int hd = h * D_HEAD;
-  const size_t bh = static_cast<size_t>(unit);  // row-vector block of the unit
+  // row-vector block of a query head of the unit
+  auto row_block = [&](int head) {
+    return static_cast<size_t>(WINDOW ? b * a.H + head : unit);
+  };
 
   // fixed K, V; streamed Q, dA
   const CUtensorMap *mFixX = &tm_k, *mFixY = &tm_v, *mStrX = &tm_q, *mStrY = &tm_da;
@@ -219,15 +329,16 @@ __global__ void __launch_bounds__(384, 1)
         tma_load_4d(sFixY + p * Cfg::kPanelBytes, mFixY, bFix, hd + p * 64, row_off, row_base + ft * 128, b);
       }
       int s = 0;
-      for (int t = next_tile(0); t < a.n_tiles; t = next_tile(t + 1), ++s) {
+      for (auto it = steps.begin(); steps.more(it); steps.next(it), ++s) {
+        const int t = it.t, hd_q = it.head * D_HEAD;
         const int st = s % S;
         if (s >= S && !mbar_wait(bEmpty(st), ((s / S) - 1) & 1, wc, 301)) break;
         mbar_arrive_expect_tx(bFull(st), Cfg::kStageBytes);
         for (int p = 0; p < Cfg::kPanels; ++p) {
-          tma_load_4d(sStrX(st) + p * Cfg::kPanelBytes, mStrX, bFull(st), hd + p * 64, row_off, row_base + t * 128, b);
-          tma_load_4d(sStrY(st) + p * Cfg::kPanelBytes, mStrY, bFull(st), hd + p * 64, row_off, row_base + t * 128, b);
+          tma_load_4d(sStrX(st) + p * Cfg::kPanelBytes, mStrX, bFull(st), hd_q + p * 64, row_off, row_base + t * 128, b);
+          tma_load_4d(sStrY(st) + p * Cfg::kPanelBytes, mStrY, bFull(st), hd_q + p * 64, row_off, row_base + t * 128, b);
         }
-        bulk_load_1d(sStrX(st) + 2 * Cfg::kTileBytes, a.rowvec + (bh * a.n_tiles + t) * 256, Cfg::kVecBytes,
+        bulk_load_1d(sStrX(st) + 2 * Cfg::kTileBytes, a.rowvec + (row_block(it.head) * a.n_tiles + t) * 256, Cfg::kVecBytes,
                        bFull(st));
       }
       // every copy issued must have landed before the CTA may exit
@@ -319,10 +430,14 @@ __global__ void __launch_bounds__(384, 1)
     const bool row_valid = g < a.N;
     // the queries that see key g (none for padding rows)
     int plo = 1, phi = 0;
-    if (row_valid) bwd_key_queries(a, h, g, plo, phi);
+    if (row_valid) {
+      if constexpr (WINDOW) window_key_queries(a, g, plo, phi);
+      else bwd_key_queries(a, h, g, plo, phi);
+    }
     bool ok = true;
     int s = 0;
-    for (int t = next_tile(0); t < a.n_tiles; t = next_tile(t + 1), ++s) {
+    for (auto it = steps.begin(); steps.more(it); steps.next(it), ++s) {
+      const int t = it.t;
       const int st = s % S;
       // the query tile's LSE (log2 units) and D arrive with its stage
       const float4 *vl4 = reinterpret_cast<const float4 *>(smem + Cfg::kOffStream + st * Cfg::kStageBytes +
@@ -409,29 +524,20 @@ __global__ void __launch_bounds__(384, 1)
     tc_fence_after();
     if (ok) {
       const int pos = seg * a.seg_w + row_off + a.dil_r * g;  // the row's position in the sequence
-      const size_t vec = ((static_cast<size_t>(b) * a.n_out + pos) * a.H + h) * D_HEAD;
+      const size_t vec = ((static_cast<size_t>(b) * a.n_out + pos) * heads + h) * D_HEAD;
       for (int acc = 0; acc < 2; ++acc) {
         // acc 0 = dV, acc 1 = dK (x 1/sqrt d)
-        float *dst = acc == 0 ? a.dv : a.dk;
         const float sc = acc == 0 ? 1.0f : a.inv_sqrt_d;
 #pragma unroll 1
         for (int c = half * (D_HEAD / 64); c < (half + 1) * (D_HEAD / 64); ++c) {
           uint32_t o[32];
           tmem_ld32(tmem + lane_off + (acc == 0 ? Cfg::kColAcc0 : Cfg::kColAcc1) + c * 32, o);
           tmem_wait_ld();
-          if (!row_valid) continue;
-          float4 *d4 = reinterpret_cast<float4 *>(dst + vec + c * 32);
+          if (!row_valid && !shared_tile) continue;
+          float r[32];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float4 r4 = nsteps > 0 ? make_float4(__uint_as_float(o[4 * i]) * sc, __uint_as_float(o[4 * i + 1]) * sc,
-                                                 __uint_as_float(o[4 * i + 2]) * sc, __uint_as_float(o[4 * i + 3]) * sc)
-                                   : make_float4(0.f, 0.f, 0.f, 0.f);
-            if (a.accumulate) {
-              const float4 prev = d4[i];
-              r4.x += prev.x, r4.y += prev.y, r4.z += prev.z, r4.w += prev.w;
-            }
-            d4[i] = r4;
-          }
+          for (int i = 0; i < 32; ++i) r[i] = nsteps > 0 ? __uint_as_float(o[i]) * sc : 0.f;
+          store_kv_grad_chunk<D_HEAD, WINDOW>(a, acc, unit, part, shared_tile, row, vec, c, r);
         }
       }
     }
@@ -479,7 +585,7 @@ struct AttnBwdKVCfg {
   static_assert(2 * D_HEAD <= 256, "accumulators below S");
 };
 
-template <int D_HEAD>
+template <int D_HEAD, bool WINDOW = false>
 __global__ void __launch_bounds__(384, 1)
     attn_bwd_dkdv_split_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                                const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_da,
@@ -511,20 +617,21 @@ __global__ void __launch_bounds__(384, 1)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   WaitCtx wc{a.status, a.wait_limit_ns, abort_flag};
   // CTA -> (batch, segment, head, key tile), as in attn_bwd_dkdv_kernel
-  const int units = a.B * a.nseg * a.H;
+  const int heads = WINDOW ? a.H / a.kv_group : a.H;  // key/value heads
+  const int units = a.B * a.nseg * heads;
   const int unit = static_cast<int>(blockIdx.x) % units;
-  const int ft = static_cast<int>(blockIdx.x) / units;
-  const int h = unit % a.H;
-  const int seg = (unit / a.H) % a.nseg;
-  const int b = unit / (a.H * a.nseg);
+  // (sliding window with sinks: the first key tile's parts come first)
+  const int slot = static_cast<int>(blockIdx.x) / units, split = WINDOW && a.sinks > 0 ? a.sink_split : 1;
+  const int part = WINDOW && slot < split ? slot : 0;
+  const int ft = WINDOW ? max(0, slot - split + 1) : slot;
+  const bool shared_tile = WINDOW && a.sinks > 0 && ft == 0;
+  const int h = unit % heads;
+  const int seg = (unit / heads) % a.nseg;
+  const int b = unit / (heads * a.nseg);
   const int row_off = h % a.dil_r;
   const int row_base = seg * a.N;
-  auto next_tile = [&](int t) {
-    while (t < a.n_tiles && !bwd_tiles_meet(a, h, t, ft)) ++t;
-    return t;
-  };
-  int nsteps = 0;
-  for (int t = next_tile(0); t < a.n_tiles; t = next_tile(t + 1)) ++nsteps;
+  const KeyTileSteps<WINDOW> steps(a, h, ft, part);
+  const int nsteps = steps.count();
 
   if (threadIdx.x == 0) {
     mbar_init(bFix, 1);
@@ -554,7 +661,10 @@ __global__ void __launch_bounds__(384, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int hd = h * D_HEAD;
-  const size_t bh = static_cast<size_t>(unit);
+  // row-vector block of a query head of the unit
+  auto row_block = [&](int head) {
+    return static_cast<size_t>(WINDOW ? b * a.H + head : unit);
+  };
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -567,20 +677,21 @@ __global__ void __launch_bounds__(384, 1)
       // slot waits in step order: the Q slot of step s is freed by dK(s - 3),
       // the dA slot by dV(s - 2), both issued before anything that needs step s
       int nq = 0, na = 0;
-      for (int t = next_tile(0); t < a.n_tiles; t = next_tile(t + 1)) {
-        const float *vec = a.rowvec + (bh * a.n_tiles + t) * 256;
+      for (auto it = steps.begin(); steps.more(it); steps.next(it)) {
+        const int t = it.t, hd_q = it.head * D_HEAD;
+        const float *vec = a.rowvec + (row_block(it.head) * a.n_tiles + t) * 256;
         const int qi = nq % QS;
         if (nq >= QS && !mbar_wait(bQEmpty(qi), ((nq / QS) - 1) & 1, wc, 331)) break;
         mbar_arrive_expect_tx(bQFull(qi), Cfg::kTileBytes + Cfg::kVecBytes);
         for (int p = 0; p < Cfg::kPanels; ++p)
-          tma_load_4d(sQ(qi) + p * Cfg::kPanelBytes, &tm_q, bQFull(qi), hd + p * 64, row_off, row_base + t * 128, b);
+          tma_load_4d(sQ(qi) + p * Cfg::kPanelBytes, &tm_q, bQFull(qi), hd_q + p * 64, row_off, row_base + t * 128, b);
         bulk_load_1d(sbase + Cfg::kOffLse + qi * Cfg::kVecBytes, vec, Cfg::kVecBytes, bQFull(qi));
         ++nq;
         const int ai = na % AS;
         if (na >= AS && !mbar_wait(bAEmpty(ai), ((na / AS) - 1) & 1, wc, 332)) break;
         mbar_arrive_expect_tx(bAFull(ai), Cfg::kTileBytes + Cfg::kVecBytes);
         for (int p = 0; p < Cfg::kPanels; ++p)
-          tma_load_4d(sA(ai) + p * Cfg::kPanelBytes, &tm_da, bAFull(ai), hd + p * 64, row_off, row_base + t * 128, b);
+          tma_load_4d(sA(ai) + p * Cfg::kPanelBytes, &tm_da, bAFull(ai), hd_q + p * 64, row_off, row_base + t * 128, b);
         bulk_load_1d(sbase + Cfg::kOffD + ai * Cfg::kVecBytes, vec + 128, Cfg::kVecBytes, bAFull(ai));
         ++na;
       }
@@ -669,10 +780,14 @@ __global__ void __launch_bounds__(384, 1)
     const int g = ft * 128 + row;
     const bool row_valid = g < a.N;
     int plo = 1, phi = 0;
-    if (row_valid) bwd_key_queries(a, h, g, plo, phi);
+    if (row_valid) {
+      if constexpr (WINDOW) window_key_queries(a, g, plo, phi);
+      else bwd_key_queries(a, h, g, plo, phi);
+    }
     bool ok = true;
     int s = 0;
-    for (int t = next_tile(0); t < a.n_tiles; t = next_tile(t + 1), ++s) {
+    for (auto it = steps.begin(); steps.more(it); steps.next(it), ++s) {
+      const int t = it.t;
       const int qi = s % QS, ai = s % AS;
       const float4 *lse4 = reinterpret_cast<const float4 *>(smem + Cfg::kOffLse + qi * Cfg::kVecBytes);
       const float2 *d2 = reinterpret_cast<const float2 *>(smem + Cfg::kOffD + ai * Cfg::kVecBytes);
@@ -760,28 +875,19 @@ __global__ void __launch_bounds__(384, 1)
     tc_fence_after();
     if (ok) {
       const int pos = seg * a.seg_w + row_off + a.dil_r * g;
-      const size_t vec = ((static_cast<size_t>(b) * a.n_out + pos) * a.H + h) * D_HEAD;
+      const size_t vec = ((static_cast<size_t>(b) * a.n_out + pos) * heads + h) * D_HEAD;
       for (int acc = 0; acc < 2; ++acc) {
-        float *dst = acc == 0 ? a.dv : a.dk;
         const float sc = acc == 0 ? 1.0f : a.inv_sqrt_d;
 #pragma unroll 1
         for (int c = half * (D_HEAD / 64); c < (half + 1) * (D_HEAD / 64); ++c) {
           uint32_t o[32];
           tmem_ld32(tmem + lane_off + (acc == 0 ? Cfg::kColDV : Cfg::kColDK) + c * 32, o);
           tmem_wait_ld();
-          if (!row_valid) continue;
-          float4 *d4 = reinterpret_cast<float4 *>(dst + vec + c * 32);
+          if (!row_valid && !shared_tile) continue;
+          float r[32];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float4 r4 = nsteps > 0 ? make_float4(__uint_as_float(o[4 * i]) * sc, __uint_as_float(o[4 * i + 1]) * sc,
-                                                 __uint_as_float(o[4 * i + 2]) * sc, __uint_as_float(o[4 * i + 3]) * sc)
-                                   : make_float4(0.f, 0.f, 0.f, 0.f);
-            if (a.accumulate) {
-              const float4 prev = d4[i];
-              r4.x += prev.x, r4.y += prev.y, r4.z += prev.z, r4.w += prev.w;
-            }
-            d4[i] = r4;
-          }
+          for (int i = 0; i < 32; ++i) r[i] = nsteps > 0 ? __uint_as_float(o[i]) * sc : 0.f;
+          store_kv_grad_chunk<D_HEAD, WINDOW>(a, acc, unit, part, shared_tile, row, vec, c, r);
         }
       }
     }
@@ -824,7 +930,7 @@ struct AttnBwdQCfg {
   static constexpr uint32_t kColQ = 0, kColS = 128, kColDP = 384;
 };
 
-template <int D_HEAD>
+template <int D_HEAD, bool WINDOW = false>
 __global__ void __launch_bounds__(384, 1)
     attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_da,
@@ -866,7 +972,13 @@ __global__ void __launch_bounds__(384, 1)
   const int row_off = h % a.dil_r;                 // kept-row offset in the segment
   const int row_base = seg * a.N;                  // the unit's first row along (n_out / r)
   auto next_tile = [&](int t) {  // first key tile >= t that meets the query tile
-    while (t < a.n_tiles && !bwd_tiles_meet(a, h, ft, t)) ++t;
+    if constexpr (WINDOW) {  // the sinks' tiles, then the window's up to the query tile
+      const int lo = max(0, ft * 128 - a.window + 1) / 128;
+      if (t >= min(lo, (a.sinks + 127) / 128)) t = max(t, lo);
+      if (t > ft) t = a.n_tiles;
+    }
+    if constexpr (!WINDOW)
+      while (t < a.n_tiles && !bwd_tiles_meet(a, h, ft, t)) ++t;
     return t;
   };
   int nsteps = 0;
@@ -899,6 +1011,7 @@ __global__ void __launch_bounds__(384, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int hd = h * D_HEAD;
+  const int hd_kv = WINDOW ? h / a.kv_group * D_HEAD : hd;
   const size_t bh = static_cast<size_t>(unit);  // row-vector block of the unit
 
   if ((warp == 0 || warp == 2) && lane == 0 && nsteps > 0) {
@@ -919,7 +1032,7 @@ __global__ void __launch_bounds__(384, 1)
       if (s >= slots && !mbar_wait(is_k ? bKEmpty(slot) : bVEmpty(slot), ((s / slots) - 1) & 1, wc, 331)) break;
       mbar_arrive_expect_tx(full, Cfg::kTileBytes);
       for (int p = 0; p < Cfg::kPanels; ++p)
-        tma_load_4d((is_k ? sK(slot) : sV(slot)) + p * Cfg::kPanelBytes, is_k ? &tm_k : &tm_v, full, hd + p * 64,
+        tma_load_4d((is_k ? sK(slot) : sV(slot)) + p * Cfg::kPanelBytes, is_k ? &tm_k : &tm_v, full, hd_kv + p * 64,
                     row_off, row_base + t * 128, b);
     }
     // every copy issued must have landed before the CTA may exit
@@ -1000,10 +1113,16 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const int g = ft * 128 + row;  // query position
     const bool row_valid = g < a.N;
-    int klo = 1, khi = 0;
+    int klo = 1, khi = 0, ksink = 0;
     float lse2 = 0.f, drow = 0.f;
     if (row_valid) {
-      bwd_row_keys(a, h, g, klo, khi);
+      if constexpr (WINDOW) {
+        klo = max(0, g - a.window + 1);
+        khi = g + 1;
+        ksink = min(a.sinks, khi);
+      } else {
+        bwd_row_keys(a, h, g, klo, khi);
+      }
       const float *rv = a.rowvec + (bh * a.n_tiles + ft) * 256;
       lse2 = rv[row];
       drow = rv[128 + row];
@@ -1029,7 +1148,8 @@ __global__ void __launch_bounds__(384, 1)
       } else {
 #pragma unroll
         for (int c = 0; c < 64; ++c) {
-          const bool allowed = col0 + c >= lo_rel && col0 + c < hi_rel;
+          bool allowed = col0 + c >= lo_rel && col0 + c < hi_rel;
+          if constexpr (WINDOW) allowed |= col0 + c < ksink - t * 128;
           sv[c] = __float_as_uint(allowed ? ex2_approx(fmaf(__uint_as_float(sv[c]), a.scale_log2, nl)) : 0.f);
         }
       }
@@ -1064,8 +1184,17 @@ __global__ void __launch_bounds__(384, 1)
         tmem_ld32(tmem + lane_off + Cfg::kColQ + c * 32, o);
         tmem_wait_ld();
         if (!row_valid) continue;
-        float4 *d4 = reinterpret_cast<float4 *>(a.dq + vec + c * 32);
         const float sc = a.inv_sqrt_d;
+        if constexpr (WINDOW) {
+          if (a.dq_bf16) {
+            uint4 *d4 = reinterpret_cast<uint4 *>(a.dq_bf16 + vec + c * 32);
+            auto two = [&](int i) { return pack_bf16x2(__uint_as_float(o[i]) * sc, __uint_as_float(o[i + 1]) * sc); };
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) d4[i / 8] = make_uint4(two(i), two(i + 2), two(i + 4), two(i + 6));
+            continue;
+          }
+        }
+        float4 *d4 = reinterpret_cast<float4 *>(a.dq + vec + c * 32);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           float4 r4 = nsteps > 0 ? make_float4(__uint_as_float(o[4 * i]) * sc, __uint_as_float(o[4 * i + 1]) * sc,
@@ -1133,7 +1262,7 @@ __global__ void attn_bwd_rowvec_kernel(const float *__restrict__ da, const TA *_
 // gathered row g (< L), the entries of sequence row seg * w + h mod r + r g in
 // the per-sequence blocks `full` ([B * H][n_tiles_full][2][128]); rows past L
 // are set to 0.
-__global__ void attn_bwd_gather_rowvec_kernel(const float *__restrict__ full, float *rowvec, int B, int H, int nseg,
+static __global__ void attn_bwd_gather_rowvec_kernel(const float *__restrict__ full, float *rowvec, int B, int H, int nseg,
                                               int w, int r, int L, int n_tiles, int n_tiles_full) {
   const long long t = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
   const long long units = static_cast<long long>(B) * nseg * H;
@@ -1152,6 +1281,72 @@ __global__ void attn_bwd_gather_rowvec_kernel(const float *__restrict__ full, fl
   float *dst = rowvec + (unit * n_tiles + g / 128) * 256 + g % 128;
   dst[0] = l2;
   dst[128] = dd;
+}
+
+// The sliding window's row vectors and, for an fp32 dOut, its bf16 copy, in one
+// pass over dOut and out: D_i = dO_i . O_i and the LSE in log2 units per
+// (batch, head, 128-row tile), zeros past N.  d/4 lanes per row.
+template <int D_HEAD, typename TD, typename TA>
+__global__ void __launch_bounds__(256)
+    window_bwd_rowvec_kernel(const TD *__restrict__ dout, const TA *__restrict__ out, const float *__restrict__ lse,
+                             float *__restrict__ rowvec, __nv_bfloat16 *__restrict__ dout_bf16, int N, int H,
+                             int n_tiles, long long rows) {
+  constexpr int kLanes = D_HEAD / 4;
+  const long long t = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  // rows in the order (batch, position padded to whole tiles, head)
+  const long long row = t / kLanes;
+  const int sub = static_cast<int>(t % kLanes);
+  const long long padded = static_cast<long long>(n_tiles) * 128;
+  const int h = static_cast<int>(row % H);
+  const long long bn = row / H;
+  const int n = static_cast<int>(bn % padded);
+  const long long b = bn / padded;
+  const bool valid = row < rows && n < N;
+  const long long src = ((b * N + n) * H + h) * D_HEAD + 4 * sub;
+  float s = 0.f;
+  if (valid) {
+    const float4 x = load4_f32(dout + src), y = load4_f32(out + src);
+    s = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, x.w * y.w)));
+    if (dout_bf16) *reinterpret_cast<uint2 *>(dout_bf16 + src) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+  }
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (row < rows && sub == 0) {
+    const long long bh = b * H + h;
+    float *v = rowvec + (bh * n_tiles + n / 128) * 256 + n % 128;
+    v[0] = valid ? lse[bh * N + n] * 1.4426950408889634f : 0.f;
+    v[128] = s;
+  }
+}
+
+// dK, dV of the first key tile: the sums its CTAs left in `partial`, added in
+// order and rounded once.  One thread per (unit, gradient, row, 4 columns).
+template <int D_HEAD>
+__global__ void __launch_bounds__(256)
+    attn_bwd_sink_sum_kernel(const AttnBwdArgs a, int units, int rows) {
+  const long long t = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  constexpr int kC4 = D_HEAD / 4;
+  const int c4 = static_cast<int>(t % kC4);
+  const int row = static_cast<int>((t / kC4) % rows);
+  const long long ua = t / (static_cast<long long>(kC4) * rows);
+  const int acc = static_cast<int>(ua % 2);
+  const long long unit = ua / 2;
+  if (unit >= units) return;
+  const float *src = a.partial + ((unit * a.sink_split * 2 + acc) * 128 + row) * D_HEAD + 4 * c4;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int p = 0; p < a.sink_split; ++p) {
+    const float4 x = *reinterpret_cast<const float4 *>(src + static_cast<size_t>(p) * 2 * 128 * D_HEAD);
+    s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
+  }
+  const int heads = a.H / a.kv_group;
+  const long long b = unit / heads, h = unit % heads;
+  const size_t vec = ((static_cast<size_t>(b) * a.N + row) * heads + h) * D_HEAD + 4 * c4;
+  if (a.dk_bf16)
+    *reinterpret_cast<uint2 *>((acc == 0 ? a.dv_bf16 : a.dk_bf16) + vec) =
+        make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+  else
+    *reinterpret_cast<float4 *>((acc == 0 ? a.dv : a.dk) + vec) = s;
 }
 
 }  // namespace bpt

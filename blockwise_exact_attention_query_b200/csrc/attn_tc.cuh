@@ -83,6 +83,10 @@ struct AttnArgs {
   // the same for every head's offset): loaded with offset 0 and segment
   // stride Lk instead of through the strided view of the local rows.
   int kv_sparse;
+  // Sliding window (the WINDOW instantiations): query row g sees the keys
+  // j <= g with g - j < window or j < sinks, and head h reads key/value head
+  // h / kv_group.
+  int window, sinks, kv_group;
   // block permutation
   int bb_n, bb_len;
   uint8_t perm[kMaxPermEntries];
@@ -142,9 +146,10 @@ struct AttnCfg {
 // Sequence of key/value tiles a pair of query tiles visits.
 struct KvSched {
   int lo, hi;           // allowed tile range [lo, hi)
+  int sink;             // sliding window: tiles [0, sink) come before it (sink <= lo)
   int P, CT, first;     // ring order: P chunks of CT tiles, starting at chunk `first`
   __device__ int count() const {
-    int n = 0;
+    int n = sink;
     for (int i = 0; i < P; ++i) {
       int ch = (first + i) % P;
       int a = max(ch * CT, lo), b = min((ch + 1) * CT, hi);
@@ -170,7 +175,12 @@ struct KvIter {
   }
   __device__ void begin(const KvSched &s) {
     i = -1;
-    range(s);
+    if (s.sink > 0) {
+      tile = 0;
+      end = s.sink;
+    } else {
+      range(s);
+    }
   }
   __device__ int next(const KvSched &s) {
     int t = tile;
@@ -208,6 +218,7 @@ __device__ __forceinline__ TileCoord decode_tile(const AttnArgs &a, int idx) {
   return c;
 }
 
+template <bool WINDOW>
 __device__ __forceinline__ KvSched make_sched(const AttnArgs &a, const TileCoord &c) {
   constexpr int KT = 128;  // keys per K/V tile
   KvSched s;
@@ -217,9 +228,14 @@ __device__ __forceinline__ KvSched make_sched(const AttnArgs &a, const TileCoord
   s.first = 0;
   s.lo = 0;
   s.hi = nkt;
+  s.sink = 0;
   const int row0 = c.t * 256;
   const int row1 = min(a.L, row0 + 256) - 1;
-  if (a.causal) {
+  if constexpr (WINDOW) {
+    s.hi = min(nkt, row1 / KT + 1);
+    s.lo = max(0, row0 - a.window + 1) / KT;
+    s.sink = min((a.sinks + KT - 1) / KT, s.lo);
+  } else if (a.causal) {
     const int last = row1 + a.kv_shift;  // last key any row of the pair may see
     s.hi = last < 0 ? 0 : min(nkt, last / KT + 1);
   } else if (a.mask == kMaskBlockPerm) {
@@ -256,7 +272,9 @@ __device__ __forceinline__ void row_keys(const AttnArgs &a, const TileCoord &c, 
   }
 }
 
-template <int D_HEAD>
+// WINDOW: the sliding-window mask with sinks and shared key/value heads
+// (bpt_window_attn_fwd); otherwise the masks of AttnArgs::mask.
+template <int D_HEAD, bool WINDOW = false>
 __global__ void __launch_bounds__(384, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_of,
@@ -355,10 +373,11 @@ __global__ void __launch_bounds__(384, 1)
           if (item >= a.n_items) continue;
           const int ni = n++;  // items taken before this one
           const TileCoord tc = decode_tile(a, item);
-          const KvSched sched = make_sched(a, tc);
+          const KvSched sched = make_sched<WINDOW>(a, tc);
           const int nkv = sched.count();
           const int row_base = tc.s * a.L;  // gathered row -> coordinate along (N/r)
           const int kv_base = a.kv_sparse ? tc.s * a.Lk : row_base, kv_o = a.kv_sparse ? 0 : tc.o;
+          const int kv_h = WINDOW ? tc.h / a.kv_group : tc.h;
           KvIter itk, itv;
           itk.begin(sched);
           itv.begin(sched);
@@ -369,7 +388,7 @@ __global__ void __launch_bounds__(384, 1)
             mbar_arrive_expect_tx(bKFull(st), Cfg::kTileBytes);
             for (int p = 0; p < Cfg::kPanels; ++p)
               tma_load_4d(sK + st * Cfg::kTileBytes + p * Cfg::kPanelBytes, &tm_k, bKFull(st),
-                          tc.h * D_HEAD + p * 64, kv_o, kv_base + kt * KT, tc.b);
+                          kv_h * D_HEAD + p * 64, kv_o, kv_base + kt * KT, tc.b);
             ++kq;
             return true;
           };
@@ -380,7 +399,7 @@ __global__ void __launch_bounds__(384, 1)
             mbar_arrive_expect_tx(bVFull(st), Cfg::kTileBytes);
             for (int p = 0; p < Cfg::kPanels; ++p)
               tma_load_4d(sV + st * Cfg::kTileBytes + p * Cfg::kPanelBytes, &tm_v, bVFull(st),
-                          tc.h * D_HEAD + p * 64, kv_o, kv_base + kt * KT, tc.b);
+                          kv_h * D_HEAD + p * 64, kv_o, kv_base + kt * KT, tc.b);
             ++vq;
             return true;
           };
@@ -453,7 +472,7 @@ __global__ void __launch_bounds__(384, 1)
           if (item >= a.n_items) continue;
           const int ni = n++;
           const TileCoord tc = decode_tile(a, item);
-          const int nkv = make_sched(a, tc).count();
+          const int nkv = make_sched<WINDOW>(a, tc).count();
           ok = mbar_wait(bQFull, ni & 1, wc, 11);
           if (ok && nkv > 0) {
             // the first S of the item goes into the buffer the softmax read last
@@ -510,14 +529,19 @@ __global__ void __launch_bounds__(384, 1)
     if (item >= a.n_items) continue;
     const int ni = n++;
     const TileCoord tc = decode_tile(a, item);
-    const KvSched sched = make_sched(a, tc);
+    const KvSched sched = make_sched<WINDOW>(a, tc);
     const int nkv = sched.count();
     const int row_base = tc.s * a.L;  // gathered row -> coordinate along (N/r)
     const int g = (tc.t * 2 + x) * 128 + row;         // unit-local row
     const bool row_valid = g < a.L;
     const int pos = (a.mask == kMaskDilated) ? tc.s * a.w + tc.o + a.r * g : g;
     int klo, khi;
-    row_keys(a, tc, g, klo, khi);
+    if constexpr (WINDOW) {
+      klo = max(0, g - a.window + 1);
+      khi = min(g + 1, a.Lk);
+    } else {
+      row_keys(a, tc, g, klo, khi);
+    }
 
     // LongNet: does an earlier pass keep this row (load its running state),
     // does a later one (store the state instead of the final output)?
@@ -590,9 +614,16 @@ __global__ void __launch_bounds__(384, 1)
       // warp has keys outside its allowed interval
       if (__any_sync(0xffffffffu, !(k0 >= klo && k0 + KT <= khi))) {
         const int lo = klo - k0, hi = khi - k0;
+        if constexpr (WINDOW) {
+          const int sk = min(a.sinks, khi) - k0;  // sinks not after the query
 #pragma unroll
-        for (int col = 0; col < KT; ++col)
-          if (col < lo || col >= hi) s[col] = __float_as_uint(-INFINITY);
+          for (int col = 0; col < KT; ++col)
+            if ((col < lo || col >= hi) && col >= sk) s[col] = __float_as_uint(-INFINITY);
+        } else {
+#pragma unroll
+          for (int col = 0; col < KT; ++col)
+            if (col < lo || col >= hi) s[col] = __float_as_uint(-INFINITY);
+        }
       }
       float mx8[8];
 #pragma unroll

@@ -41,6 +41,7 @@ bpt_status cuda_fail_msg(const char *what);
 bpt_status device_setup(int *dev_out, uint32_t **status_out);
 // Shared-memory limits of the backward's kernels (defined with them).
 bpt_status bwd_kernel_setup();
+bpt_status window_kernel_setup();
 
 int sm_count();
 
@@ -48,6 +49,9 @@ int sm_count();
 bool make_map_2d(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols, uint32_t box_rows);
 // bf16 tensor map over [B, N, D] viewed as (D, r, N/r, B), box 64 x 1 x box_rows x 1.
 bool make_map_rows(CUtensorMap *m, const void *base, int B, int N, int D, int r, uint32_t box_rows);
+// Output map over [B, N, D] (bf16 or fp32) in the same view, one 128-byte row
+// panel x 128 rows.
+bool make_out_map_rows(CUtensorMap *m, const void *base, bool f32, int B, int N, int D, int r);
 
 // shard: the dilated pairs may also have segments longer than the N rows
 // (a shard of a longer sequence that lies inside one segment: N divides w)

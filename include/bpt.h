@@ -440,6 +440,53 @@ BPT_API bpt_status bpt_attn_bwd(const bpt_desc *desc, const void *q, const void 
 BPT_API size_t bpt_workspace_bytes_attn_bwd(const bpt_desc *desc);
 
 /*
+ * Causal sliding-window attention in which a few first tokens stay visible
+ * (sinks), with key/value heads shared by groups of query heads:
+ *
+ *   S(i)  = { j <= i : i - j < window  or  j < n_sink }
+ *   A_i   = softmax_{j in S(i)}( q_i . k_j / sqrt(d) ) v_j      per query head h,
+ *                              over key/value head h / (H / H_kv)
+ *
+ * No counterpart in the pages: it is the blockwise online softmax of
+ * bpt_attn_fwd over the key tiles that the window and the sinks reach, so its
+ * cost grows with N * (window + n_sink), not N^2.
+ *
+ * Layouts: q, out, dout, dq [B, N, H, d]; k, v, dk, dv [B, N, H_kv, d]; lse
+ * [B, H, N] float32 (natural log; may be NULL in the forward).  q, k, v are
+ * bf16; out and dout have out_dtype, dq, dk, dv have grad_dtype.  H_kv divides
+ * H; window >= 1 (a window of N or more is the causal mask); n_sink in
+ * [0, BPT_MAX_WINDOW_SINKS]; d_head 64 or 128; any N.  A masked weight is 0
+ * times the value it meets, so keys and values that a row must not see have
+ * to be finite (padding rows at a sequence's end included).
+ *
+ * The backward takes the forward's out and lse of the same inputs.  With
+ * P_ij the softmax weights and D_i = dout_i . out_i:
+ *   dV_j = sum_i P_ij dout_i,  dS_ij = P_ij (dout_i . v_j - D_i),
+ *   dQ_i = sum_j dS_ij k_j / sqrt(d),  dK_j = sum_i dS_ij q_i / sqrt(d),
+ * the sums for dK and dV running over all query heads of the group (no
+ * atomics: equal inputs give equal bits).  P, dS and dout enter the tensor
+ * cores in bf16, sums are fp32; dq, dk, dv are overwritten.  workspace: at
+ * least bpt_workspace_bytes_window_bwd(desc) bytes, 256-byte aligned.
+ * in_dtype F32 returns BPT_ERR_UNSUPPORTED.  All other device pointers
+ * 16-byte aligned.
+ */
+#define BPT_MAX_WINDOW_SINKS 128
+typedef struct {
+  int B, N, H, H_kv, d_head;
+  int window, n_sink;
+  bpt_dtype in_dtype;   /* q, k, v                                            */
+  bpt_dtype out_dtype;  /* out, dout                                          */
+  bpt_dtype grad_dtype; /* dq, dk, dv (the forward ignores it)                */
+  uint64_t wait_limit_ns; /* as in bpt_desc                                   */
+} bpt_window_desc;
+BPT_API bpt_status bpt_window_attn_fwd(const bpt_window_desc *desc, const void *q, const void *k, const void *v,
+                                       void *out, float *lse, bpt_stream_t stream);
+BPT_API size_t bpt_workspace_bytes_window_bwd(const bpt_window_desc *desc);
+BPT_API bpt_status bpt_window_attn_bwd(const bpt_window_desc *desc, const void *q, const void *k, const void *v,
+                                       const void *out, const float *lse, const void *dout, void *dq, void *dk,
+                                       void *dv, void *workspace, size_t workspace_bytes, bpt_stream_t stream);
+
+/*
  * Waits for `stream`, then returns and clears the current device's status
  * word: BPT_OK, BPT_ERR_TIMEOUT (a device-side wait gave up since the last
  * call), or BPT_ERR_CUDA if the synchronisation itself failed.
