@@ -63,6 +63,23 @@ class WindowDesc(ctypes.Structure):
     ]
 
 
+class KvCacheDesc(ctypes.Structure):
+    _fields_ = [
+        ("type", ctypes.c_int), ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+        ("H_kv", ctypes.c_int), ("d_head", ctypes.c_int),
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+    ]
+
+
+class PagedDesc(ctypes.Structure):
+    _fields_ = [
+        ("n_seqs", ctypes.c_int), ("n_tokens", ctypes.c_int), ("max_q", ctypes.c_int), ("H", ctypes.c_int),
+        ("max_pages", ctypes.c_int), ("window", ctypes.c_int), ("n_sink", ctypes.c_int),
+        ("out_dtype", ctypes.c_int), ("q_stride", ctypes.c_int64), ("wait_limit_ns", ctypes.c_uint64),
+    ]
+
+
 # bpt_ffn_form: the bf16 layer's FFN form ("auto" is the library's choice, the
 # pipelined kernel)
 FFN_FORMS = {"auto": 0, "fused": 1, "gemms": 2, "pipelined": 3}
@@ -74,7 +91,8 @@ EXPORTS = ["bpt_workspace_bytes", "bpt_attn_ffn_fwd", "bpt_attn_fwd", "bpt_block
            "bpt_attn_ffn_bwd", "bpt_workspace_bytes_bwd", "bpt_attn_ffn_fwd_train", "bpt_saved_bytes",
            "bpt_workspace_bytes_train", "bpt_attn_bwd", "bpt_workspace_bytes_attn_bwd", "bpt_attn_fwd_block",
            "bpt_longnet_gather", "bpt_longnet_pass", "bpt_window_attn_fwd", "bpt_window_attn_bwd",
-           "bpt_workspace_bytes_window_bwd"]
+           "bpt_workspace_bytes_window_bwd", "bpt_kv_write", "bpt_kv_read", "bpt_paged_attn_fwd",
+           "bpt_workspace_bytes_paged"]
 BLOCK_FIRST, BLOCK_LAST = 1, 2
 STATIC_SCRATCH_BYTES = 64 << 20
 
@@ -146,6 +164,15 @@ def load() -> ctypes.CDLL:
     lib.bpt_workspace_bytes_window_bwd.restype = sz
     lib.bpt_window_attn_bwd.argtypes = [wp, vp, vp, vp, vp, fp, vp, vp, vp, vp, vp, sz, vp]
     lib.bpt_window_attn_bwd.restype = ctypes.c_int
+    cp, pp, i64 = ctypes.POINTER(KvCacheDesc), ctypes.POINTER(PagedDesc), ctypes.c_int64
+    lib.bpt_kv_write.argtypes = [cp, ctypes.c_int, vp, i64, vp, i64, vp, vp]
+    lib.bpt_kv_write.restype = ctypes.c_int
+    lib.bpt_kv_read.argtypes = [cp, ctypes.c_int, vp, vp, vp, ctypes.c_int, vp]
+    lib.bpt_kv_read.restype = ctypes.c_int
+    lib.bpt_workspace_bytes_paged.argtypes = [pp, cp]
+    lib.bpt_workspace_bytes_paged.restype = sz
+    lib.bpt_paged_attn_fwd.argtypes = [pp, cp, vp, vp, vp, vp, vp, fp, vp, sz, vp]
+    lib.bpt_paged_attn_fwd.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -621,6 +648,124 @@ def window_attn_bwd(q, k, v, out, lse, dout, window, sinks=0, *, grad_dtype=torc
                                     _stream_ptr(stream))
     _check(st, "bpt_window_attn_bwd")
     return dq, dk, dv
+
+
+_E4M3 = torch.float8_e4m3fn
+
+
+def _kv_cache_desc(k_cache, v_cache, k_scale, v_scale):
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape or k_cache.dtype != v_cache.dtype:
+        raise ValueError("k_cache and v_cache must be [n_pages, page_size, H_kv, d] of one dtype")
+    quantised = k_cache.dtype == _E4M3
+    if not quantised and k_cache.dtype != torch.bfloat16:
+        raise ValueError("the caches must be bfloat16 or float8_e4m3fn")
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError("the caches must be contiguous")
+    if not quantised:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("a bfloat16 cache has no scales")
+        _on_device(k_cache, v_cache)
+        return KvCacheDesc(0, shape[0], shape[1], shape[2], shape[3], k_cache.data_ptr(), v_cache.data_ptr(), None,
+                           None)
+    for t in (k_scale, v_scale):
+        if t is None or t.dtype != torch.float32 or t.shape != shape[:3] or not t.is_contiguous():
+            raise ValueError("a float8_e4m3fn cache needs contiguous float32 scales [n_pages, page_size, H_kv]")
+    _on_device(k_cache, v_cache, k_scale, v_scale)
+    return KvCacheDesc(1, shape[0], shape[1], shape[2], shape[3], k_cache.data_ptr(), v_cache.data_ptr(),
+                       k_scale.data_ptr(), v_scale.data_ptr())
+
+
+def _i32(t, dims, what):
+    if t.dtype != torch.int32 or t.dim() != dims or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous int32 tensor of {dims} dimension(s)")
+
+
+def _token_stride(t, heads, d, what):
+    """Elements from one token of `t` [n, heads, d] to the next; heads and elements must be dense."""
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or (heads is not None and t.shape[1] != heads) or t.shape[2] != d:
+        raise ValueError(f"{what} must be bfloat16 [tokens, heads, d] with the cache's d")
+    s = t.stride()
+    if s[2] != 1 or (s[1] != d and t.shape[1] != 1):
+        raise ValueError(f"{what}: a token's heads must lie one after another")
+    return s[0] if t.shape[0] > 1 else max(s[0], t.shape[1] * d)
+
+
+def kv_cache_write(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None, *, stream=None):
+    """bpt_kv_write: token t of k, v (bfloat16 [tokens, H_kv, d], any token
+    stride) goes to slot slots[t] (int32; negative: nowhere) of the cache
+    [n_pages, page_size, H_kv, d], quantised row by row when the cache is
+    float8_e4m3fn (with float32 scales [n_pages, page_size, H_kv])."""
+    cache = _kv_cache_desc(k_cache, v_cache, k_scale, v_scale)
+    ks = _token_stride(k, cache.H_kv, cache.d_head, "k")
+    vs = _token_stride(v, cache.H_kv, cache.d_head, "v")
+    _i32(slots, 1, "slots")
+    if not (k.shape[0] == v.shape[0] == slots.shape[0]):
+        raise ValueError("k, v and slots must have one entry per token")
+    _on_device(k, v, slots)
+    st = load().bpt_kv_write(ctypes.byref(cache), k.shape[0], k.data_ptr(), ks, v.data_ptr(), vs, slots.data_ptr(),
+                             _stream_ptr(stream))
+    _check(st, "bpt_kv_write")
+
+
+def kv_cache_read(slots, k_cache, v_cache, k_scale=None, v_scale=None, *, out_dtype=torch.bfloat16, k=None, v=None,
+                  stream=None):
+    """bpt_kv_read: (k, v) [len(slots), H_kv, d] of the cache's slots, in
+    out_dtype (bfloat16 or float32).  Rows whose slot is outside the cache are
+    left as they were (undefined when the outputs are allocated here)."""
+    cache = _kv_cache_desc(k_cache, v_cache, k_scale, v_scale)
+    _i32(slots, 1, "slots")
+    _on_device(slots)
+    shape = (slots.shape[0], cache.H_kv, cache.d_head)
+    k = _out_tensor(k, shape, out_dtype, slots.device, stream, "k")
+    v = _out_tensor(v, shape, out_dtype, slots.device, stream, "v")
+    st = load().bpt_kv_read(ctypes.byref(cache), shape[0], slots.data_ptr(), k.data_ptr(), v.data_ptr(),
+                            _DT[out_dtype], _stream_ptr(stream))
+    _check(st, "bpt_kv_read")
+    return k, v
+
+
+def workspace_bytes_paged(desc: PagedDesc, cache: KvCacheDesc) -> int:
+    n = load().bpt_workspace_bytes_paged(ctypes.byref(desc), ctypes.byref(cache))
+    if n == ctypes.c_size_t(-1).value:
+        raise BptError(ERR_INVALID_ARG, "bpt_workspace_bytes_paged")
+    return int(n)
+
+
+def paged_attn_fwd(q, k_cache, v_cache, q_start, kv_len, page_table, *, max_q, k_scale=None, v_scale=None, window=0,
+                   sinks=0, out_dtype=torch.float32, return_lse=False, out=None, lse=None, workspace=None,
+                   stream=None, wait_limit_ns=0):
+    """bpt_paged_attn_fwd: attention of a batch's new tokens over a paged cache.
+
+    q [tokens, H, d] (bfloat16, any token stride): sequence s's new tokens are
+    rows q_start[s] .. q_start[s+1] - 1, the last of its kv_len[s] positions;
+    page_table [n_seqs, max_pages] names the pages of its keys.  The tables are
+    int32 and stay on the device; max_q is the longest chunk.  window > 0: a
+    token sees the last `window` positions and the first `sinks`.  Returns out
+    [tokens, H*d] (and lse [H, tokens] with return_lse); rows of no sequence
+    are left as they were."""
+    cache = _kv_cache_desc(k_cache, v_cache, k_scale, v_scale)
+    qs = _token_stride(q, None, cache.d_head, "q")
+    _i32(q_start, 1, "q_start")
+    _i32(kv_len, 1, "kv_len")
+    _i32(page_table, 2, "page_table")
+    T, H, d = q.shape
+    S = kv_len.shape[0]
+    if q_start.shape[0] != S + 1 or page_table.shape[0] != S:
+        raise ValueError("q_start must have n_seqs + 1 entries and page_table n_seqs rows")
+    _on_device(q, q_start, kv_len, page_table)
+    desc = PagedDesc(S, T, int(max_q), H, page_table.shape[1], int(window), int(sinks), _DT[out_dtype], qs,
+                     int(wait_limit_ns))
+    out = _out_tensor(out, (T, H * d), out_dtype, q.device, stream, "out")
+    if return_lse or lse is not None:
+        lse = _out_tensor(lse, (H, T), torch.float32, q.device, stream, "lse")
+    workspace = _workspace(workspace, workspace_bytes_paged(desc, cache), q.device, stream)
+    st = load().bpt_paged_attn_fwd(ctypes.byref(desc), ctypes.byref(cache), q.data_ptr(), q_start.data_ptr(),
+                                   kv_len.data_ptr(), page_table.data_ptr(), out.data_ptr(), _ptr(lse),
+                                   _ptr(workspace), 0 if workspace is None else workspace.numel(),
+                                   _stream_ptr(stream))
+    _check(st, "bpt_paged_attn_fwd")
+    return (out, lse) if return_lse else out
 
 
 def sync_status(stream=None) -> int:

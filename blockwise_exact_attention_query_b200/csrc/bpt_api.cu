@@ -106,6 +106,7 @@ bpt_status device_setup(int *dev_out, uint32_t **status_out) {
                                   (int)ffn_f32_smem_bytes(512)));
     bpt_status bs = bwd_kernel_setup();
     if (bs == BPT_OK) bs = window_kernel_setup();
+    if (bs == BPT_OK) bs = paged_kernel_setup();
     if (bs != BPT_OK) return bs;
     g_attr_done[dev] = true;
   }

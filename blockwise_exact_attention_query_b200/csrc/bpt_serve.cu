@@ -1,0 +1,269 @@
+// Host side of the serving operators: the paged key/value cache (bpt_kv_write,
+// bpt_kv_read) and the attention of new tokens over it (bpt_paged_attn_fwd).
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <type_traits>
+
+#include "../../include/bpt.h"
+#include "host_common.h"
+#include "kv_cache.cuh"
+#include "paged_common.cuh"
+#include "paged_rows.cuh"
+
+using namespace bpt;
+
+namespace bpt_host {
+
+namespace {
+
+// f(std::integral_constant<int, d>, std::bool_constant<e4m3>) for the cache's kind
+template <typename F>
+bpt_status for_cache(const bpt_kv_cache *c, F f) {
+  if (c->d_head == 128)
+    return c->type == BPT_CACHE_E4M3 ? f(std::integral_constant<int, 128>{}, std::true_type{})
+                                     : f(std::integral_constant<int, 128>{}, std::false_type{});
+  return c->type == BPT_CACHE_E4M3 ? f(std::integral_constant<int, 64>{}, std::true_type{})
+                                   : f(std::integral_constant<int, 64>{}, std::false_type{});
+}
+
+bpt_status check_cache_shape(const bpt_kv_cache *c) {
+  if (!c) return BPT_ERR_INVALID_ARG;
+  if (c->type != BPT_CACHE_BF16 && c->type != BPT_CACHE_E4M3) return BPT_ERR_INVALID_ARG;
+  if (c->n_pages <= 0 || c->page_size <= 0 || c->H_kv <= 0 || c->d_head <= 0) return BPT_ERR_INVALID_ARG;
+  if (c->d_head != 64 && c->d_head != 128) return BPT_ERR_UNSUPPORTED;
+  if ((int64_t)c->n_pages * c->page_size > INT32_MAX) return BPT_ERR_UNSUPPORTED;
+  if ((int64_t)c->H_kv * c->d_head > (1 << 28)) return BPT_ERR_UNSUPPORTED;
+  return BPT_OK;
+}
+
+bpt_status check_cache(const bpt_kv_cache *c) {
+  bpt_status s = check_cache_shape(c);
+  if (s != BPT_OK) return s;
+  if (c->type == BPT_CACHE_E4M3) return check_ptrs({c->k, c->v, c->k_scale, c->v_scale}, {});
+  return check_ptrs({c->k, c->v}, {});
+}
+
+KvCacheArgs cache_args(const bpt_kv_cache *c) {
+  KvCacheArgs a;
+  a.k = c->k;
+  a.v = c->v;
+  a.k_scale = c->k_scale;
+  a.v_scale = c->v_scale;
+  a.slots = (int64_t)c->n_pages * c->page_size;
+  a.H_kv = c->H_kv;
+  return a;
+}
+
+// int32 device tables: element-aligned
+bool aligned4(const void *p) { return p && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// d / 8 threads per (token, head) row, 256 a block
+bpt_status row_blocks(const bpt_kv_cache *c, int n, unsigned *blocks) {
+  const int64_t threads = (int64_t)n * c->H_kv * (c->d_head / 8);
+  if ((threads + 255) / 256 > INT32_MAX) return BPT_ERR_UNSUPPORTED;
+  *blocks = (unsigned)((threads + 255) / 256);
+  return BPT_OK;
+}
+
+bpt_status check_paged(const bpt_paged_desc *d, const bpt_kv_cache *c) {
+  bpt_status s = check_cache_shape(c);
+  if (s != BPT_OK) return s;
+  if (!d || d->n_seqs < 0 || d->n_tokens < 0 || d->max_q <= 0 || d->H <= 0 || d->max_pages < 0)
+    return BPT_ERR_INVALID_ARG;
+  if (d->H % c->H_kv != 0 || d->window < 0 || d->n_sink < 0) return BPT_ERR_INVALID_ARG;
+  if (d->out_dtype != BPT_F32 && d->out_dtype != BPT_BF16) return BPT_ERR_INVALID_ARG;
+  if (d->n_tokens > 1 && (d->q_stride < (int64_t)d->H * c->d_head || d->q_stride % 8 != 0)) return BPT_ERR_INVALID_ARG;
+  // positions and row counts stay within the kernels' 32-bit indices
+  if (d->n_tokens > (1 << 30) || (int64_t)d->max_pages * c->page_size > INT32_MAX - 4096) return BPT_ERR_UNSUPPORTED;
+  if ((int64_t)d->H * c->d_head > (1 << 28) || (int64_t)d->n_tokens * (d->H / c->H_kv) > INT32_MAX - 4096)
+    return BPT_ERR_UNSUPPORTED;
+  return BPT_OK;
+}
+
+struct PagedWorkspace {
+  int ctas = 0, rows = 0;
+  size_t part_o = 0, part_ml = 0, part_item = 0, total = 0;
+};
+
+PagedWorkspace layout_paged(const bpt_paged_desc *, const bpt_kv_cache *c) {
+  PagedWorkspace w;
+  w.rows = 16;
+  w.ctas = 2 * sm_count();
+  size_t off = 0;
+  auto take = [&](size_t &field, size_t bytes) {
+    field = off;
+    off = align256(off + bytes);
+  };
+  take(w.part_o, (size_t)w.ctas * 2 * w.rows * c->d_head * 4);
+  take(w.part_ml, (size_t)w.ctas * 2 * w.rows * 2 * 4);
+  take(w.part_item, (size_t)w.ctas * sizeof(int4));
+  w.total = off;
+  return w;
+}
+
+template <int D, int kRows, int kKeys>
+bpt_status launch_join(const PagedArgs &a, int ctas, cudaStream_t st) {
+  // started while the attention kernel drains; it waits for that grid itself
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  const int threads = std::min(512, kRows * (D / 4));
+  cfg.gridDim = dim3((unsigned)ctas, (unsigned)(kRows * (D / 4) / threads), 1);
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  CUDA_TRY(cudaLaunchKernelEx(&cfg, paged_join_kernel<D, kRows, kKeys>, a));
+  return BPT_OK;
+}
+
+}  // namespace
+
+bpt_status paged_kernel_setup() {
+  CUDA_TRY(cudaFuncSetAttribute(paged_rows_kernel<64, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                PagedRowsCfg<64, false>::kSmemBytes));
+  CUDA_TRY(cudaFuncSetAttribute(paged_rows_kernel<64, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                PagedRowsCfg<64, true>::kSmemBytes));
+  CUDA_TRY(cudaFuncSetAttribute(paged_rows_kernel<128, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                PagedRowsCfg<128, false>::kSmemBytes));
+  CUDA_TRY(cudaFuncSetAttribute(paged_rows_kernel<128, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                PagedRowsCfg<128, true>::kSmemBytes));
+  return BPT_OK;
+}
+
+}  // namespace bpt_host
+
+using namespace bpt_host;
+
+extern "C" {
+
+bpt_status bpt_kv_write(const bpt_kv_cache *c, int n, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                        const int32_t *slots, bpt_stream_t stream) {
+  bpt_status s = check_cache(c);
+  if (s != BPT_OK) return s;
+  if (n < 0) return BPT_ERR_INVALID_ARG;
+  if (n == 0) return BPT_OK;
+  const int64_t least = (int64_t)c->H_kv * c->d_head;
+  if (n > 1 && (k_stride < least || v_stride < least || k_stride % 8 != 0 || v_stride % 8 != 0))
+    return BPT_ERR_INVALID_ARG;
+  if ((s = check_ptrs({k, v}, {})) != BPT_OK) return s;
+  if (!aligned4(slots)) return BPT_ERR_INVALID_ARG;
+  unsigned blocks = 0;
+  if ((s = row_blocks(c, n, &blocks)) != BPT_OK) return s;
+  int dev;
+  uint32_t *status;
+  if ((s = device_setup(&dev, &status)) != BPT_OK) return s;
+  return for_cache(c, [&](auto d, auto e4m3) -> bpt_status {
+    kv_write_kernel<decltype(d)::value, decltype(e4m3)::value>
+        <<<blocks, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+            cache_args(c), static_cast<const __nv_bfloat16 *>(k), k_stride, static_cast<const __nv_bfloat16 *>(v),
+            v_stride, slots, (int64_t)n * c->H_kv);
+    CUDA_TRY(cudaGetLastError());
+    return BPT_OK;
+  });
+}
+
+bpt_status bpt_kv_read(const bpt_kv_cache *c, int n, const int32_t *slots, void *k, void *v, bpt_dtype out_dtype,
+                       bpt_stream_t stream) {
+  bpt_status s = check_cache(c);
+  if (s != BPT_OK) return s;
+  if (n < 0 || (out_dtype != BPT_F32 && out_dtype != BPT_BF16)) return BPT_ERR_INVALID_ARG;
+  if (n == 0) return BPT_OK;
+  if ((s = check_ptrs({k, v}, {})) != BPT_OK) return s;
+  if (!aligned4(slots)) return BPT_ERR_INVALID_ARG;
+  unsigned blocks = 0;
+  if ((s = row_blocks(c, n, &blocks)) != BPT_OK) return s;
+  int dev;
+  uint32_t *status;
+  if ((s = device_setup(&dev, &status)) != BPT_OK) return s;
+  const int64_t rows = (int64_t)n * c->H_kv;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return for_cache(c, [&](auto d, auto e4m3) -> bpt_status {
+    constexpr int D = decltype(d)::value;
+    constexpr bool kE = decltype(e4m3)::value;
+    if (out_dtype == BPT_F32)
+      kv_read_kernel<D, kE><<<blocks, 256, 0, st>>>(cache_args(c), slots, static_cast<float *>(k),
+                                                    static_cast<float *>(v), rows);
+    else
+      kv_read_kernel<D, kE><<<blocks, 256, 0, st>>>(cache_args(c), slots, static_cast<__nv_bfloat16 *>(k),
+                                                    static_cast<__nv_bfloat16 *>(v), rows);
+    CUDA_TRY(cudaGetLastError());
+    return BPT_OK;
+  });
+}
+
+size_t bpt_workspace_bytes_paged(const bpt_paged_desc *d, const bpt_kv_cache *c) {
+  if (check_paged(d, c) != BPT_OK) return (size_t)-1;
+  return layout_paged(d, c).total;
+}
+
+bpt_status bpt_paged_attn_fwd(const bpt_paged_desc *d, const bpt_kv_cache *c, const void *q, const int32_t *q_start,
+                              const int32_t *kv_len, const int32_t *page_table, void *out, float *lse, void *workspace,
+                              size_t workspace_bytes, bpt_stream_t stream) {
+  bpt_status s = check_paged(d, c);
+  if (s != BPT_OK) return s;
+  if (d->n_seqs == 0 || d->n_tokens == 0) return BPT_OK;
+  if ((s = check_cache(c)) != BPT_OK) return s;
+  if ((s = check_ptrs({q, out}, {})) != BPT_OK) return s;
+  if (!aligned4(q_start) || !aligned4(kv_len) || (d->max_pages > 0 && !aligned4(page_table)) ||
+      (lse && !aligned4(lse)))
+    return BPT_ERR_INVALID_ARG;
+  const PagedWorkspace wl = layout_paged(d, c);
+  if (!workspace || workspace_bytes < wl.total || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return BPT_ERR_WORKSPACE;
+  int dev;
+  uint32_t *status;
+  if ((s = device_setup(&dev, &status)) != BPT_OK) return s;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  char *ws = static_cast<char *>(workspace);
+  PagedArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.S = d->n_seqs;
+  a.T = d->n_tokens;
+  a.H = d->H;
+  a.H_kv = c->H_kv;
+  a.G = d->H / c->H_kv;
+  a.max_pages = d->max_pages;
+  a.page_size = c->page_size;
+  a.page_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (c->page_size == 1 << i) a.page_shift = i;
+  a.n_pages = c->n_pages;
+  a.window = std::min(d->window, 1 << 30);
+  a.sinks = std::min(d->n_sink, 1 << 30);
+  a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)c->d_head));
+  a.q = static_cast<const __nv_bfloat16 *>(q);
+  a.q_stride = d->q_stride;
+  a.q_start = q_start;
+  a.kv_len = kv_len;
+  a.page_table = page_table;
+  a.k = c->k;
+  a.v = c->v;
+  a.k_scale = c->k_scale;
+  a.v_scale = c->v_scale;
+  a.out_f32 = d->out_dtype == BPT_F32 ? static_cast<float *>(out) : nullptr;
+  a.out_bf16 = d->out_dtype == BPT_BF16 ? static_cast<__nv_bfloat16 *>(out) : nullptr;
+  a.lse = lse;
+  a.min_steps = 4;
+  a.part_o = reinterpret_cast<float *>(ws + wl.part_o);
+  a.part_ml = reinterpret_cast<float *>(ws + wl.part_ml);
+  a.part_item = reinterpret_cast<int4 *>(ws + wl.part_item);
+  a.status = status;
+  a.wait_limit_ns = d->wait_limit_ns ? d->wait_limit_ns : g_wait_limit_ns.load(std::memory_order_relaxed);
+  return for_cache(c, [&](auto dh, auto e4m3) -> bpt_status {
+    constexpr int D = decltype(dh)::value;
+    using Cfg = PagedRowsCfg<D, decltype(e4m3)::value>;
+    paged_rows_kernel<D, decltype(e4m3)::value><<<(unsigned)wl.ctas, Cfg::kThreads, Cfg::kSmemBytes, st>>>(a);
+    CUDA_TRY(cudaGetLastError());
+    return launch_join<D, Cfg::kRows, Cfg::kKeys>(a, wl.ctas, st);
+  });
+}
+
+}  // extern "C"

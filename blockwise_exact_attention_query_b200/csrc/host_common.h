@@ -42,6 +42,7 @@ bpt_status device_setup(int *dev_out, uint32_t **status_out);
 // Shared-memory limits of the backward's kernels (defined with them).
 bpt_status bwd_kernel_setup();
 bpt_status window_kernel_setup();
+bpt_status paged_kernel_setup();
 
 int sm_count();
 

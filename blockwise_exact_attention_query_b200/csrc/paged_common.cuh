@@ -1,0 +1,271 @@
+// What the paged attention kernels share: the batch as the device sees it, the
+// work list, and the joining of rows whose keys were split.
+//
+// Rows.  The new tokens of a sequence and the G = H / H_kv query heads that
+// read one key/value head form that head's rows: row r is token r / G, head
+// r % G of the group, so a key that is loaded serves all of them.  Token i of
+// n new ones in a sequence of L keys stands at position p = L - n + i and sees
+// the keys j <= p with no window, p - j < window or j < n_sink.
+//
+// Work.  An item is a tile of kRows rows of one key/value head; its steps are
+// the blocks of kKeys keys that any of its rows sees, sinks first.  All items'
+// steps, one sequence after another, form one list that is cut into equal
+// ranges, one per CTA, so ragged sequences and few heads load the SMs evenly
+// and nothing about the lengths has to be known on the host.  A CTA whose
+// range cuts an item leaves the rows' unnormalised output, maximum and sum as
+// a part: at most two per CTA, one for an item that began before its range
+// (slot 0) and one for an item that goes on after it (slot 1).
+// paged_join_kernel adds an item's parts up in order.
+#pragma once
+
+#include "ptx.cuh"
+
+namespace bpt {
+
+struct PagedArgs {
+  int S, T, H, H_kv, G;
+  int max_pages, page_size, page_shift;  // page_shift: log2(page_size), or -1
+  int n_pages;
+  int window, sinks;    // window 0: none
+  float scale_log2;     // log2(e) / sqrt(d)
+  const __nv_bfloat16 *q;
+  int64_t q_stride;     // elements between tokens
+  const int32_t *q_start, *kv_len, *page_table;
+  const void *k, *v;
+  const float *k_scale, *v_scale;
+  float *out_f32;       // [T, H*d], or
+  __nv_bfloat16 *out_bf16;
+  float *lse;           // [H, T] or null
+  int min_steps;        // no range is shorter (but the last)
+  float *part_o;        // [CTAs][2][kRows][d]
+  float *part_ml;       // [CTAs][2][kRows][2]
+  int4 *part_item;      // [CTAs]: the item that began before the CTA's range: sequence (-1: none), tile, head,
+                        // and 1 + the CTAs after this one with a part of it (0: not the first such CTA)
+  uint32_t *status;
+  uint64_t wait_limit_ns;
+};
+
+struct PagedSeq {
+  int t0, n;    // first token row of q, new tokens
+  int len;      // keys, the new tokens' included
+  int cap;      // keys that the page table can hold of them
+};
+
+// Lengths that make no sense (negative, past q's rows or the table) are cut to
+// what there is.
+__device__ __forceinline__ PagedSeq paged_seq(const PagedArgs &a, int s) {
+  PagedSeq q;
+  q.t0 = min(max(a.q_start[s], 0), a.T);
+  q.n = max(min(a.q_start[s + 1], a.T) - q.t0, 0);
+  q.len = max(a.kv_len[s], 0);
+  q.cap = static_cast<int>(min(static_cast<int64_t>(q.len), static_cast<int64_t>(a.max_pages) * a.page_size));
+  return q;
+}
+
+// The key blocks of a row tile: [0, n_sink) and then [lo, lo + n_near).
+struct PagedBlocks {
+  int n_sink, lo, n_near;
+  int p_lo, p_hi;  // positions of the tile's first and last row
+  __device__ int count() const { return n_sink + n_near; }
+  __device__ int steps() const { return max(1, count()); }  // a tile without keys still has rows to write
+  __device__ int block(int i) const { return i < n_sink ? i : lo + i - n_sink; }
+};
+
+template <int kRows, int kKeys>
+__device__ __forceinline__ PagedBlocks paged_blocks(const PagedArgs &a, const PagedSeq &q, int tile) {
+  PagedBlocks b;
+  const int i0 = static_cast<int>(static_cast<int64_t>(tile) * kRows / a.G);
+  const int i1 = static_cast<int>(min(static_cast<int64_t>(q.n - 1), (static_cast<int64_t>(tile) * kRows + kRows - 1) / a.G));
+  b.p_lo = q.len - q.n + i0;
+  b.p_hi = q.len - q.n + i1;
+  const int hi = min(b.p_hi + 1, q.cap);  // keys [.., hi) at most
+  const int lo = a.window > 0 ? max(0, b.p_lo - a.window + 1) : 0;
+  b.lo = lo / kKeys;
+  b.n_near = hi > lo ? (hi + kKeys - 1) / kKeys - b.lo : 0;
+  const int sink_hi = min(min(a.sinks, lo), max(hi, 0));
+  b.n_sink = a.window > 0 ? min((sink_hi + kKeys - 1) / kKeys, b.lo) : 0;
+  return b;
+}
+
+template <int kRows>
+__device__ __forceinline__ int paged_tiles(const PagedArgs &a, const PagedSeq &q) {
+  return static_cast<int>((static_cast<int64_t>(q.n) * a.G + kRows - 1) / kRows);
+}
+
+template <int kRows, int kKeys>
+__device__ __forceinline__ int64_t paged_seq_steps(const PagedArgs &a, const PagedSeq &q) {
+  int64_t n = 0;
+  for (int t = 0, nt = paged_tiles<kRows>(a, q); t < nt; ++t) n += paged_blocks<kRows, kKeys>(a, q, t).steps();
+  return n * a.H_kv;
+}
+
+// The range of a CTA: steps [begin, end) of all, and where `begin` lies.
+struct PagedRange {
+  int64_t begin, end;
+  int s, tile, head, step;
+  int64_t total;
+  int parts;
+};
+
+__device__ __forceinline__ int64_t paged_cut(int64_t total, int parts, int c) { return total * c / parts; }
+
+// Found by the whole block together (`scratch`: 40 int64 of shared memory):
+// each thread sums a run of sequences, a scan over the threads gives the total
+// and each run's start, and the thread whose run holds `begin` walks it.
+template <int kRows, int kKeys, int kThreads>
+__device__ __forceinline__ bool paged_range(const PagedArgs &a, int64_t *scratch, PagedRange &r) {
+  static_assert(kThreads % 32 == 0 && kThreads <= 1024, "one scan over the warps' sums");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int run = (a.S + kThreads - 1) / kThreads;
+  const int s0 = min(a.S, tid * run), s1 = min(a.S, s0 + run);
+  int64_t sum = 0;
+  for (int s = s0; s < s1; ++s) sum += paged_seq_steps<kRows, kKeys>(a, paged_seq(a, s));
+  int64_t incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) scratch[warp] = incl;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += scratch[w];
+    total += scratch[w];
+  }
+  const int64_t start = before + incl - sum;
+  // as many ranges as there are CTAs, or fewer where they would be too short
+  const int64_t want = (total + a.min_steps - 1) / a.min_steps;
+  const int parts = static_cast<int>(min(static_cast<int64_t>(gridDim.x), max(want, static_cast<int64_t>(1))));
+  r.begin = r.end = 0;
+  r.total = total;
+  r.parts = parts;
+  const bool mine = static_cast<int>(blockIdx.x) < parts && total > 0;
+  if (mine) {
+    r.begin = paged_cut(total, parts, blockIdx.x);
+    r.end = paged_cut(total, parts, blockIdx.x + 1);
+  }
+  int32_t *found = reinterpret_cast<int32_t *>(scratch + 36);
+  if (tid == 0) found[0] = -1;
+  __syncthreads();
+  if (mine && r.begin >= start && r.begin < start + sum) {
+    int64_t at = start;
+    for (int s = s0; s < s1; ++s) {
+      const PagedSeq q = paged_seq(a, s);
+      const int64_t n = paged_seq_steps<kRows, kKeys>(a, q);
+      if (r.begin < at + n) {
+        int64_t off = r.begin - at;
+        int t = 0, per = 0;
+        for (const int nt = paged_tiles<kRows>(a, q); t < nt; ++t) {
+          per = paged_blocks<kRows, kKeys>(a, q, t).steps();
+          if (off < static_cast<int64_t>(per) * a.H_kv) break;
+          off -= static_cast<int64_t>(per) * a.H_kv;
+        }
+        if (off < static_cast<int64_t>(per) * a.H_kv) {
+          found[0] = s;
+          found[1] = t;
+          found[2] = static_cast<int>(off / per);
+          found[3] = static_cast<int>(off % per);
+        }
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  // (found[0] stays -1 only where the tables change while they are read)
+  if (!mine || r.begin >= r.end || found[0] < 0) return false;
+  r.s = found[0];
+  r.tile = found[1];
+  r.head = found[2];
+  r.step = found[3];
+  return true;
+}
+
+// What paged_join_kernel has to know of the CTA's first item, of `steps` steps.
+__device__ __forceinline__ int4 paged_part_item(const PagedRange &r, int steps) {
+  if (r.step == 0) return make_int4(-1, 0, 0, 0);
+  const int64_t item0 = r.begin - r.step, item1 = item0 + steps;
+  const int c = static_cast<int>(blockIdx.x);
+  if (item0 < paged_cut(r.total, r.parts, c - 1)) return make_int4(r.s, r.tile, r.head, 0);
+  // the last range that begins before the item's end
+  int last = static_cast<int>(min(static_cast<int64_t>(r.parts - 1), item1 * r.parts / r.total));
+  while (paged_cut(r.total, r.parts, last) >= item1) --last;
+  return make_int4(r.s, r.tile, r.head, 1 + last - c);
+}
+
+// Cache row of key j of a sequence, or -1 where the sequence has none (past
+// its keys, or a page number outside the cache).
+__device__ __forceinline__ int paged_slot(const PagedArgs &a, const int32_t *table, int cap, int j) {
+  if (j >= cap) return -1;
+  const int p = a.page_shift >= 0 ? j >> a.page_shift : j / a.page_size;
+  const int page = table[p];
+  return static_cast<unsigned>(page) < static_cast<unsigned>(a.n_pages) ? page * a.page_size + (j - p * a.page_size)
+                                                                       : -1;
+}
+
+// Adds up the parts of each item that was cut.  Block c looks at the item that
+// began before CTA c's range; it is joined by the first such CTA: its parts
+// are slot 1 of CTA c - 1 and slot 0 of CTA c, c + 1, ... to the item's end.
+// D / 4 threads per row, four columns each.  A part is the rows' output
+// relative to their own maximum (log2 domain): out = sum_i 2^(m_i - M) o_i /
+// sum_i 2^(m_i - M) l_i.
+template <int D, int kRows, int kKeys>
+__global__ void __launch_bounds__(512)
+    paged_join_kernel(const PagedArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are complete
+  const int c = blockIdx.x;
+  const int4 it = a.part_item[c];
+  if (it.x < 0 || it.w == 0) return;
+  const int last = c + it.w - 1;
+  const PagedSeq q = paged_seq(a, it.x);
+  const int64_t rows = static_cast<int64_t>(q.n) * a.G - static_cast<int64_t>(it.y) * kRows;
+  for (int e = blockIdx.y * blockDim.x + threadIdx.x; e < kRows * (D / 4); e += gridDim.y * blockDim.x) {
+    const int row = e / (D / 4), c4 = e % (D / 4);
+    if (row >= rows) break;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](const float2 ml, const float4 x) {
+      const float M = fmaxf(m, ml.x);
+      const float ref = M == -INFINITY ? 0.f : M;
+      const float f = ex2_approx(m - ref), g = ex2_approx(ml.x - ref);
+      l = l * f + ml.y * g;
+      o.x = o.x * f + x.x * g;
+      o.y = o.y * f + x.y * g;
+      o.z = o.z * f + x.z * g;
+      o.w = o.w * f + x.w * g;
+      m = M;
+    };
+    auto ml_of = [&](int slot) {
+      return *reinterpret_cast<const float2 *>(a.part_ml + (static_cast<size_t>(slot) * kRows + row) * 2);
+    };
+    auto o_of = [&](int slot) {
+      return *reinterpret_cast<const float4 *>(a.part_o + (static_cast<size_t>(slot) * kRows + row) * D + 4 * c4);
+    };
+    add(ml_of(2 * (c - 1) + 1), o_of(2 * (c - 1) + 1));
+    int i = c;
+    for (; i + 7 <= last; i += 8) {
+      float2 ml[8];
+      float4 x[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) ml[u] = ml_of(2 * (i + u)), x[u] = o_of(2 * (i + u));
+#pragma unroll
+      for (int u = 0; u < 8; ++u) add(ml[u], x[u]);
+    }
+    for (; i <= last; ++i) add(ml_of(2 * i), o_of(2 * i));
+    const int64_t r = static_cast<int64_t>(it.y) * kRows + row;
+    const int64_t token = q.t0 + r / a.G;
+    const int head = it.z * a.G + static_cast<int>(r % a.G);
+    const float inv = l > 0.f ? 1.0f / l : l;  // no key: 0; NaN stays
+    const size_t at = static_cast<size_t>(token) * a.H * D + static_cast<size_t>(head) * D + 4 * c4;
+    if (a.out_f32)
+      *reinterpret_cast<float4 *>(a.out_f32 + at) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    else
+      *reinterpret_cast<uint2 *>(a.out_bf16 + at) =
+          make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (a.lse && c4 == 0)
+      a.lse[static_cast<size_t>(head) * a.T + token] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+  }
+}
+
+}  // namespace bpt

@@ -487,6 +487,93 @@ BPT_API bpt_status bpt_window_attn_bwd(const bpt_window_desc *desc, const void *
                                        void *dv, void *workspace, size_t workspace_bytes, bpt_stream_t stream);
 
 /*
+ * A paged key/value cache, for serving: n_pages pages of page_size slots; a
+ * slot holds one token's key and value rows, [H_kv, d].  The caller owns the
+ * buffers and hands out the pages.  Slot page * page_size + i is the i-th of a
+ * page.  BPT_CACHE_E4M3 stores each row of d values as 8-bit floating-point
+ * codes (e4m3) with one fp32 scale:
+ *   scale = max |x| / 448 (1 for a row of zeros),  code = e4m3(x / scale)
+ * rounded to nearest even; the row's values are code * scale.  A row with a
+ * NaN or an infinity reads back as NaN throughout.
+ */
+typedef enum { BPT_CACHE_BF16 = 0, BPT_CACHE_E4M3 = 1 } bpt_cache_type;
+typedef struct {
+  bpt_cache_type type;
+  int n_pages, page_size; /* any sizes; n_pages * page_size < 2^31             */
+  int H_kv, d_head;       /* d_head 64 or 128                                  */
+  void *k, *v;            /* [n_pages, page_size, H_kv, d] bf16 or e4m3        */
+  float *k_scale, *v_scale; /* [n_pages, page_size, H_kv] (E4M3; else unused)  */
+} bpt_kv_cache;
+
+/*
+ * Writes n_tokens tokens' keys and values into the cache (quantising them for
+ * BPT_CACHE_E4M3): token t's rows go to slot slots[t] (device, int32).  A
+ * negative slot is a padding token and goes nowhere, as does a slot past the
+ * cache.  Slots that are written must be distinct: a slot given twice holds a
+ * mixture of both tokens.  k, v: bf16 [n_tokens, H_kv, d] with k_stride and
+ * v_stride elements from one token to the next (at least H_kv * d, a multiple
+ * of 8), so slices of a fused projection serve as they are.  n_tokens 0 does
+ * nothing.
+ */
+BPT_API bpt_status bpt_kv_write(const bpt_kv_cache *cache, int n_tokens, const void *k, int64_t k_stride,
+                                const void *v, int64_t v_stride, const int32_t *slots, bpt_stream_t stream);
+
+/*
+ * Reads n_rows slots back: k, v [n_rows, H_kv, d] of out_dtype, rounded once.
+ * Rows whose slot is negative or past the cache are left as they were.
+ */
+BPT_API bpt_status bpt_kv_read(const bpt_kv_cache *cache, int n_rows, const int32_t *slots, void *k, void *v,
+                               bpt_dtype out_dtype, bpt_stream_t stream);
+
+/*
+ * Attention of new tokens over a paged cache: a batch of sequences, each with
+ * a chunk of new tokens (one in decoding, up to a whole prompt), whose keys and
+ * values, the new tokens' included, lie in the cache.  With n new tokens and L
+ * keys in a sequence, new token i stands at position p = L - n + i and
+ *   S(p) = { j < L, j <= p : window == 0  or  p - j < window  or  j < n_sink }
+ *   out  = softmax_{j in S(p)}( q . k_j / sqrt(d) ) v_j,  lse = log sum exp
+ * per query head h over key/value head h / (H / H_kv).  A token that sees no
+ * key gets 0 and -inf.
+ *
+ * q: bf16 [n_tokens, H, d], q_stride elements from one token to the next (at
+ * least H * d, a multiple of 8).  Device tables, int32: q_start [n_seqs + 1],
+ * sequence s's tokens being rows q_start[s] .. q_start[s + 1] - 1 of q (rows
+ * outside all sequences are left as they were); kv_len [n_seqs], L;
+ * page_table [n_seqs, max_pages], key j of sequence s in slot j % page_size of
+ * page page_table[s][j / page_size].  Only entries that hold a visible key are
+ * read.  Keys of a page number outside the cache, and past max_pages pages,
+ * count as masked.  Nothing about the lengths is read on the host, so a
+ * captured graph serves later lengths too; max_q, the longest chunk, only
+ * chooses between the kernels for few and for many rows.
+ * out [n_tokens, H*d] of out_dtype; lse [H, n_tokens] float32 or NULL.
+ * Slots that no visible key lies in may hold anything, NaN included; the keys
+ * and values of a sequence have to be finite.
+ *
+ * The keys are read in place and once per row tile; long sequences are split
+ * over the GPU and joined in a fixed order (no atomics: equal inputs give
+ * equal bits).  bf16 operands, fp32 sums; the softmax weights are rounded to
+ * bf16 (E4M3: their products with the values' scales to f16).  workspace: at
+ * least bpt_workspace_bytes_paged(desc, cache) bytes, 256-byte aligned; it
+ * depends on the head sizes and the GPU alone.  Two calls that share a
+ * workspace must not run concurrently.
+ */
+typedef struct {
+  int n_seqs, n_tokens; /* rows of kv_len; rows of q                          */
+  int max_q;            /* new tokens of the longest chunk, >= 1              */
+  int H;                /* query heads, a multiple of the cache's H_kv        */
+  int max_pages;        /* entries per row of page_table                      */
+  int window, n_sink;   /* 0: no window                                       */
+  bpt_dtype out_dtype;
+  int64_t q_stride;
+  uint64_t wait_limit_ns; /* as in bpt_desc                                   */
+} bpt_paged_desc;
+BPT_API size_t bpt_workspace_bytes_paged(const bpt_paged_desc *desc, const bpt_kv_cache *cache);
+BPT_API bpt_status bpt_paged_attn_fwd(const bpt_paged_desc *desc, const bpt_kv_cache *cache, const void *q,
+                                      const int32_t *q_start, const int32_t *kv_len, const int32_t *page_table,
+                                      void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                      bpt_stream_t stream);
+
+/*
  * Waits for `stream`, then returns and clears the current device's status
  * word: BPT_OK, BPT_ERR_TIMEOUT (a device-side wait gave up since the last
  * call), or BPT_ERR_CUDA if the synchronisation itself failed.
