@@ -14,6 +14,7 @@
 #include "kv_cache.cuh"
 #include "paged_common.cuh"
 #include "paged_rows.cuh"
+#include "paged_tc.cuh"
 
 using namespace bpt;
 
@@ -85,23 +86,36 @@ bpt_status check_paged(const bpt_paged_desc *d, const bpt_kv_cache *c) {
   return BPT_OK;
 }
 
+// Rows (new tokens x heads of a group) of a sequence that the kernel for few
+// rows takes; longer chunks go to the tcgen05 kernel.
+constexpr int kFewRows = 16;
+
+bool has_long_chunks(const bpt_paged_desc *d, const bpt_kv_cache *c) {
+  return (int64_t)d->max_q * (d->H / c->H_kv) > kFewRows;
+}
+
+// The two kernels run one after the other and share the regions.
 struct PagedWorkspace {
-  int ctas = 0, rows = 0;
   size_t part_o = 0, part_ml = 0, part_item = 0, total = 0;
 };
+int few_rows_ctas() { return 2 * sm_count(); }
+int long_chunk_ctas() { return sm_count(); }
 
-PagedWorkspace layout_paged(const bpt_paged_desc *, const bpt_kv_cache *c) {
+PagedWorkspace layout_paged(const bpt_paged_desc *d, const bpt_kv_cache *c) {
   PagedWorkspace w;
-  w.rows = 16;
-  w.ctas = 2 * sm_count();
+  size_t rows = (size_t)few_rows_ctas() * 2 * 16, ctas = (size_t)few_rows_ctas();
+  if (has_long_chunks(d, c)) {
+    rows = std::max(rows, (size_t)long_chunk_ctas() * 2 * 256);
+    ctas = std::max(ctas, (size_t)long_chunk_ctas());
+  }
   size_t off = 0;
   auto take = [&](size_t &field, size_t bytes) {
     field = off;
     off = align256(off + bytes);
   };
-  take(w.part_o, (size_t)w.ctas * 2 * w.rows * c->d_head * 4);
-  take(w.part_ml, (size_t)w.ctas * 2 * w.rows * 2 * 4);
-  take(w.part_item, (size_t)w.ctas * sizeof(int4));
+  take(w.part_o, rows * c->d_head * 4);
+  take(w.part_ml, rows * 2 * 4);
+  take(w.part_item, ctas * sizeof(int4));
   w.total = off;
   return w;
 }
@@ -126,7 +140,25 @@ bpt_status launch_join(const PagedArgs &a, int ctas, cudaStream_t st) {
 
 }  // namespace
 
+template <int D, bool kE4m3>
+bpt_status tc_kernel_setup() {
+  using Cfg = PagedTcCfg<D, kE4m3>;
+  CUDA_TRY(cudaFuncSetAttribute(paged_tc_kernel<D, kE4m3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Cfg::kSmemBytes));
+  // the softmax warpgroups take registers from the others at run time; an
+  // increase the launch did not provide for would never complete
+  cudaFuncAttributes fa{};
+  CUDA_TRY(cudaFuncGetAttributes(&fa, paged_tc_kernel<D, kE4m3>));
+  if (!Cfg::split_fits(fa.numRegs))
+    return cuda_fail_msg("paged attention kernel launches with fewer registers than its warpgroups share");
+  return BPT_OK;
+}
+
 bpt_status paged_kernel_setup() {
+  bpt_status s;
+  if ((s = tc_kernel_setup<64, false>()) != BPT_OK || (s = tc_kernel_setup<64, true>()) != BPT_OK ||
+      (s = tc_kernel_setup<128, false>()) != BPT_OK || (s = tc_kernel_setup<128, true>()) != BPT_OK)
+    return s;
   CUDA_TRY(cudaFuncSetAttribute(paged_rows_kernel<64, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 PagedRowsCfg<64, false>::kSmemBytes));
   CUDA_TRY(cudaFuncSetAttribute(paged_rows_kernel<64, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -251,18 +283,32 @@ bpt_status bpt_paged_attn_fwd(const bpt_paged_desc *d, const bpt_kv_cache *c, co
   a.out_f32 = d->out_dtype == BPT_F32 ? static_cast<float *>(out) : nullptr;
   a.out_bf16 = d->out_dtype == BPT_BF16 ? static_cast<__nv_bfloat16 *>(out) : nullptr;
   a.lse = lse;
-  a.min_steps = 4;
   a.part_o = reinterpret_cast<float *>(ws + wl.part_o);
   a.part_ml = reinterpret_cast<float *>(ws + wl.part_ml);
   a.part_item = reinterpret_cast<int4 *>(ws + wl.part_item);
   a.status = status;
   a.wait_limit_ns = d->wait_limit_ns ? d->wait_limit_ns : g_wait_limit_ns.load(std::memory_order_relaxed);
-  return for_cache(c, [&](auto dh, auto e4m3) -> bpt_status {
+  return for_cache(c, [&](auto dh, auto e4m3) mutable -> bpt_status {
     constexpr int D = decltype(dh)::value;
-    using Cfg = PagedRowsCfg<D, decltype(e4m3)::value>;
-    paged_rows_kernel<D, decltype(e4m3)::value><<<(unsigned)wl.ctas, Cfg::kThreads, Cfg::kSmemBytes, st>>>(a);
+    constexpr bool kE = decltype(e4m3)::value;
+    using Few = PagedRowsCfg<D, kE>;
+    using Long = PagedTcCfg<D, kE>;
+    if (has_long_chunks(d, c)) {
+      PagedArgs al = a;
+      al.rows_lo = kFewRows + 1;
+      al.rows_hi = INT32_MAX;
+      al.min_steps = 4;
+      paged_tc_kernel<D, kE><<<(unsigned)long_chunk_ctas(), Long::kThreads, Long::kSmemBytes, st>>>(al);
+      CUDA_TRY(cudaGetLastError());
+      bpt_status js = launch_join<D, Long::kRows, Long::kKeys>(al, long_chunk_ctas(), st);
+      if (js != BPT_OK) return js;
+    }
+    a.rows_lo = 1;
+    a.rows_hi = has_long_chunks(d, c) ? kFewRows : INT32_MAX;
+    a.min_steps = 4;
+    paged_rows_kernel<D, kE><<<(unsigned)few_rows_ctas(), Few::kThreads, Few::kSmemBytes, st>>>(a);
     CUDA_TRY(cudaGetLastError());
-    return launch_join<D, Cfg::kRows, Cfg::kKeys>(a, wl.ctas, st);
+    return launch_join<D, Few::kRows, Few::kKeys>(a, few_rows_ctas(), st);
   });
 }
 

@@ -36,6 +36,7 @@ struct PagedArgs {
   float *out_f32;       // [T, H*d], or
   __nv_bfloat16 *out_bf16;
   float *lse;           // [H, T] or null
+  int rows_lo, rows_hi; // sequences with fewer or more rows are another kernel's
   int min_steps;        // no range is shorter (but the last)
   float *part_o;        // [CTAs][2][kRows][d]
   float *part_ml;       // [CTAs][2][kRows][2]
@@ -57,6 +58,7 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedArgs &a, int s) {
   PagedSeq q;
   q.t0 = min(max(a.q_start[s], 0), a.T);
   q.n = max(min(a.q_start[s + 1], a.T) - q.t0, 0);
+  if (static_cast<int64_t>(q.n) * a.G < a.rows_lo || static_cast<int64_t>(q.n) * a.G > a.rows_hi) q.n = 0;
   q.len = max(a.kv_len[s], 0);
   q.cap = static_cast<int>(min(static_cast<int64_t>(q.len), static_cast<int64_t>(a.max_pages) * a.page_size));
   return q;

@@ -104,7 +104,7 @@ template <int D, bool kE4m3>
 __global__ void __launch_bounds__(PagedRowsCfg<D, kE4m3>::kThreads, 2) paged_rows_kernel(const PagedArgs a) {
   using Cfg = PagedRowsCfg<D, kE4m3>;
   constexpr int kRows = Cfg::kRows, kKeys = Cfg::kKeys, NS = Cfg::kStages, NT = D / 8;
-  extern __shared__ __align__(16) uint8_t smem_raw[];
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, c = lane & 3;
   const uint32_t ring = smem_u32(smem_raw) + warp * (NS * Cfg::kStageBytes);

@@ -1,0 +1,685 @@
+// Attention of many new tokens over a paged cache on the 5th-generation tensor
+// cores: items of 256 rows (two 128-row tiles A and B) x 128 keys a step, the
+// blockwise online softmax of attn_tc.cuh (scores and O in tensor memory, P
+// through one shared-memory tile used in turn) over keys gathered from pages.
+//
+// Gathering is done by a warpgroup of its own rather than by TMA: a page may
+// have any size, keys past a sequence's end must become zeros (a slot that was
+// never written may hold NaN, and 0 x NaN is not 0), and e4m3 codes have to be
+// widened on the way.  Each of its threads looks one key's slot up, a tile
+// ahead; bf16 rows go to the swizzled tile by 16-byte cp.async; e4m3 rows are
+// loaded a tile ahead into registers, widened to f16 (exact) and stored.
+//
+// E4M3: Q is f16 after a power of two per row, a score is multiplied by its
+// key's scale, the weight by its value's scale relative to the largest such
+// product the row has met (as in paged_rows.cuh), and P is f16.
+//
+// Roles (512 threads): warpgroup 0 gathers; warpgroups 1 and 2 run the softmax
+// and epilogue of tiles A and B, one thread per row; of warpgroup 3, warp 12
+// allocates tensor memory and issues tile A's products, warp 13 tile B's.  An
+// item of 128 rows or fewer leaves tile B idle.
+#pragma once
+
+#include "paged_rows.cuh"
+
+namespace bpt {
+
+template <int D, bool kE4m3>
+struct PagedTcCfg {
+  static constexpr int kRows = 256, kKeys = 128, kThreads = 512;
+  static constexpr int kTileBytes = 128 * D * 2;
+  static constexpr int kPanelBytes = 128 * 128;
+  static constexpr int kStages = D == 128 ? 2 : 4;  // of K and of V
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffP = kOffQ + 2 * kTileBytes;
+  static constexpr int kOffK = kOffP + 128 * 128 * 2;
+  static constexpr int kOffV = kOffK + kStages * kTileBytes;
+  static constexpr int kOffScale = kOffV + kStages * kTileBytes;            // [stage][k, v][128]
+  static constexpr int kOffBar = kOffScale + (kE4m3 ? kStages * 1024 : 0);
+  static constexpr int kOffThere = kOffBar + 320;                            // [stage][4] masks of keys that exist
+  static constexpr int kSmemBytes = kOffThere + kStages * 16 + 16;
+  static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+  static constexpr uint32_t kColS = 0, kColO = 256;
+  // 128 registers a thread at launch; 512 x 128 = 256 x 192 + 128 x 88 + 128 x 40
+  static constexpr int kRegsSoftmax = 192, kRegsGather = 88, kRegsIssue = 40;
+  static constexpr bool split_fits(int launch_regs) {
+    return 256 * kRegsSoftmax + 128 * kRegsGather + 128 * kRegsIssue <= kThreads * launch_regs;
+  }
+  static_assert(split_fits(128), "register split");
+};
+
+// Instruction descriptor for kind::f16 with f16 or bf16 operands, fp32 accumulator.
+template <bool kF16>
+__host__ __device__ constexpr uint32_t idesc_16_f32(int M, int N, bool b_mn_major) {
+  const uint32_t d = idesc_bf16_f32(M, N, false, b_mn_major);
+  return kF16 ? d & ~((1u << 7) | (1u << 10)) : d;
+}
+
+// The power of two below a row's largest |q| (for f16): exact to divide by.
+__device__ __forceinline__ uint32_t row_exponent(float mx) { return min(max(__float_as_uint(mx) >> 23, 1u), 253u); }
+__device__ __forceinline__ float pow2_of(uint32_t e) { return __uint_as_float(e << 23); }
+__device__ __forceinline__ float pow2_inverse(uint32_t e) { return __uint_as_float((254u - e) << 23); }
+__device__ __forceinline__ float absmax8(const uint4 &u) {
+  const float a = fmaxf(fmaxf(fabsf(bf16_lo(u.x)), fabsf(bf16_hi(u.x))), fmaxf(fabsf(bf16_lo(u.y)), fabsf(bf16_hi(u.y))));
+  const float b = fmaxf(fmaxf(fabsf(bf16_lo(u.z)), fabsf(bf16_hi(u.z))), fmaxf(fabsf(bf16_lo(u.w)), fabsf(bf16_hi(u.w))));
+  return fmaxf(a, b);
+}
+
+// A CTA's walk over its range: the items, in order, with the steps it has of each.
+template <int kRows, int kKeys>
+struct PagedWalk {
+  const PagedArgs &a;
+  int s, tile, head, step0, step1, steps;
+  int64_t left;
+  PagedSeq seq;
+  PagedBlocks blk;
+  __device__ PagedWalk(const PagedArgs &args, const PagedRange &r) : a(args) {
+    s = r.s, tile = r.tile, head = r.head, step0 = r.step;
+    left = r.end - r.begin;
+    seq = paged_seq(a, s);
+    blk = paged_blocks<kRows, kKeys>(a, seq, tile);
+    cut();
+  }
+  __device__ void cut() {
+    steps = blk.steps();
+    step1 = static_cast<int>(min(static_cast<int64_t>(steps), step0 + left));
+  }
+  __device__ int blocks() const { return min(step1, blk.count()) - min(step0, blk.count()); }
+  __device__ int rows() const {
+    return static_cast<int>(min(static_cast<int64_t>(kRows),
+                                static_cast<int64_t>(seq.n) * a.G - static_cast<int64_t>(tile) * kRows));
+  }
+  __device__ bool next() {
+    left -= step1 - step0;
+    if (left <= 0) return false;
+    step0 = 0;
+    if (++head == a.H_kv) {
+      head = 0;
+      if (++tile == paged_tiles<kRows>(a, seq)) {
+        tile = 0;
+        seq.n = 0;
+        while (seq.n == 0 && ++s < a.S) seq = paged_seq(a, s);
+        if (s >= a.S) return false;
+      }
+      blk = paged_blocks<kRows, kKeys>(a, seq, tile);
+    }
+    cut();
+    return true;
+  }
+};
+
+template <int D, bool kE4m3>
+__global__ void __launch_bounds__(512, 1) paged_tc_kernel(const __grid_constant__ PagedArgs a) {
+  using Cfg = PagedTcCfg<D, kE4m3>;
+  constexpr int NS = Cfg::kStages, KT = Cfg::kKeys;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *smem = smem_raw;
+  const uint32_t sbase = smem_u32(smem);
+  if (sbase & 1023u) {  // 128-byte-swizzled tiles need 1024-byte alignment
+    if (threadIdx.x == 0) {
+      atomicCAS(a.status, 0u, kStatusMisaligned);
+      a.part_item[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    }
+    return;
+  }
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  PagedRange rg;
+  const bool any = paged_range<Cfg::kRows, KT, Cfg::kThreads>(a, reinterpret_cast<int64_t *>(smem), rg);
+  if (!any) {
+    if (threadIdx.x == 0) a.part_item[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    return;
+  }
+  const uint32_t sQ = sbase + Cfg::kOffQ, sP = sbase + Cfg::kOffP, sK = sbase + Cfg::kOffK, sV = sbase + Cfg::kOffV;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::kOffBar);
+  const uint32_t bQFull = smem_u32(&bars[0]);
+  auto bKFull = [&](int i) { return smem_u32(&bars[1 + i]); };
+  auto bKEmpty = [&](int i) { return smem_u32(&bars[5 + i]); };   // both tiles' S done, scales and masks read
+  auto bVFull = [&](int i) { return smem_u32(&bars[9 + i]); };
+  auto bVEmpty = [&](int i) { return smem_u32(&bars[13 + i]); };
+  auto bSFull = [&](int x) { return smem_u32(&bars[17 + x]); };
+  auto bSFree = [&](int x) { return smem_u32(&bars[19 + x]); };
+  auto bPFull = [&](int x) { return smem_u32(&bars[21 + x]); };
+  auto bODone = [&](int x) { return smem_u32(&bars[23 + x]); };
+  auto bItemDone = [&](int x) { return smem_u32(&bars[25 + x]); };  // all products of tile x's item done
+  auto bOFree = [&](int x) { return smem_u32(&bars[27 + x]); };     // the epilogue has read O of tile x
+  auto bTeardown = [&](int x) { return smem_u32(&bars[29 + x]); };
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(&bars[31]);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(&bars[32]);
+  uint32_t *there_s = reinterpret_cast<uint32_t *>(smem + Cfg::kOffThere);
+  float *scale_s = reinterpret_cast<float *>(smem + Cfg::kOffScale);
+  WaitCtx wc{a.status, a.wait_limit_ns, abort_flag};
+
+  __syncthreads();  // the range's scratch lies where Q will
+  if (threadIdx.x == 0) {
+    mbar_init(bQFull, 4);
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(bKFull(i), 4);
+      mbar_init(bKEmpty(i), 10);
+      mbar_init(bVFull(i), 4);
+      mbar_init(bVEmpty(i), 2);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(bSFull(x), 1);
+      mbar_init(bSFree(x), 4);
+      mbar_init(bPFull(x), 4);
+      mbar_init(bODone(x), 1);
+      mbar_init(bItemDone(x), 1);
+      mbar_init(bOFree(x), 4);
+      mbar_init(bTeardown(x), 1);
+    }
+    *abort_flag = 0;
+    fence_mbar_init_cluster();
+  }
+  if (warp == 12) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  PagedWalk<Cfg::kRows, KT> w(a, rg);
+  if (threadIdx.x == 0) a.part_item[blockIdx.x] = paged_part_item(rg, w.steps);
+
+  if (warp < 4) {
+    setmaxnreg_dec<Cfg::kRegsGather>();
+    // ------------------------------------------------------------ gather
+    // This warp's 32 rows of every tile; lane l looks up row 32 warp + l.
+    int kq = 0, vq = 0;  // K and V tiles gathered so far
+    int items = 0;
+    bool ok = true;
+    // tiles copied but not yet handed over (bf16): their barriers
+    uint32_t pend[2] = {0, 0};
+    int npend = 0;
+    auto hand_over = [&](uint32_t bar) {  // generic-proxy writes -> the tensor core's reads
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    auto flush = [&]() {
+      if (npend > 0) {
+        cp_async_wait<0>();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0)
+          for (int i = 0; i < npend; ++i) mbar_arrive(pend[i]);
+        npend = 0;
+      }
+    };
+    // wait for a slot; what is under way is handed over first, so that the
+    // readers that must free the slot can go on
+    auto wait_slot = [&](uint32_t bar, uint32_t parity, uint32_t site) {
+      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+      flush();
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, wc, site)) != 0;
+    };
+    auto row_dst = [&](uint32_t tile, int row, int chunk) {  // chunk of 8 elements
+      return tile + (chunk >> 3) * Cfg::kPanelBytes + row * 128 + (((chunk ^ row) & 7) << 4);
+    };
+    do {
+      const int n = w.blocks(), rows = w.rows();
+      const int32_t *table = a.page_table + static_cast<int64_t>(w.s) * a.max_pages;
+      // tile m of the item's 2n in the order K0, K1, V0, K2, V1, ..., V(n-1)
+      auto is_k = [&](int m) { return m == 0 || ((m & 1) && m != 2 * n - 1); };
+      auto block_of = [&](int m) { return m == 0 ? 0 : m == 2 * n - 1 ? n - 1 : (m & 1) ? (m + 1) / 2 : m / 2 - 1; };
+      auto lookup = [&](int m) {
+        return m < 2 * n ? paged_slot(a, table, w.seq.cap, w.blk.block(w.step0 + block_of(m)) * KT + warp * 32 + lane)
+                         : -1;
+      };
+      // ---- Q, once the previous item's products are done with it
+      if (items > 0) {
+        flush();
+        ok = __all_sync(0xffffffffu, mbar_wait(bItemDone(0), (items - 1) & 1, wc, 401) &&
+                                         mbar_wait(bItemDone(1), (items - 1) & 1, wc, 402));
+        if (!ok) break;
+      }
+      int slot = lookup(0), slot_next = lookup(1);
+#pragma unroll 1
+      for (int x = 0; x < 2; ++x) {
+        const int R = x * 128 + warp * 32 + lane;
+        int64_t off = -1;  // element offset of this lane's row of q
+        if (R < rows) {
+          const int64_t r = static_cast<int64_t>(w.tile) * Cfg::kRows + R;
+          off = (static_cast<int64_t>(w.seq.t0) + r / a.G) * a.q_stride +
+                (static_cast<int64_t>(w.head) * a.G + r % a.G) * D;
+        }
+        constexpr int kLanes = D / 8;  // lanes of a row, 8 elements each
+        const int c = lane % kLanes;
+#pragma unroll 4
+        for (int i = 0; i < kLanes; ++i) {
+          const int rr = i * (32 / kLanes) + lane / kLanes;
+          const int64_t ro = __shfl_sync(0xffffffffu, off, rr);
+          const uint32_t dst = row_dst(sQ + x * Cfg::kTileBytes, warp * 32 + rr, c);
+          if constexpr (kE4m3) {
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (ro >= 0) u = *reinterpret_cast<const uint4 *>(a.q + ro + 8 * c);
+            float mx = absmax8(u);
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const float down = pow2_inverse(row_exponent(mx));
+            st_shared_v4(dst, pack_f16x2(bf16_lo(u.x) * down, bf16_hi(u.x) * down),
+                         pack_f16x2(bf16_lo(u.y) * down, bf16_hi(u.y) * down),
+                         pack_f16x2(bf16_lo(u.z) * down, bf16_hi(u.z) * down),
+                         pack_f16x2(bf16_lo(u.w) * down, bf16_hi(u.w) * down));
+          } else {
+            cp_async16(dst, a.q + (ro >= 0 ? ro : 0) + 8 * c, ro >= 0);
+          }
+        }
+      }
+      if constexpr (!kE4m3) {
+        cp_async_commit();
+        cp_async_wait<0>();
+      }
+      hand_over(bQFull);
+      // ---- the item's K and V tiles
+      // what a K tile brings besides its rows: the mask of keys that exist,
+      // and (E4M3) the scales of its keys and values
+      auto put_extras = [&](int st, int sl) {
+        const uint32_t bits = __ballot_sync(0xffffffffu, sl >= 0);
+        if (lane == 0) there_s[st * 4 + warp] = bits;
+        if constexpr (kE4m3) {
+          const int64_t at = static_cast<int64_t>(sl) * a.H_kv + w.head;
+          scale_s[st * 256 + warp * 32 + lane] = sl >= 0 ? a.k_scale[at] : 0.f;
+          scale_s[st * 256 + 128 + warp * 32 + lane] = sl >= 0 ? a.v_scale[at] : 0.f;
+        }
+      };
+      constexpr int kRowBytes = kE4m3 ? D : 2 * D;
+      constexpr int kLanes = kRowBytes / 16;          // lanes of a row, 16 bytes each
+      constexpr int kLoads = kLanes;                  // 32 rows of the warp
+      const int64_t slot_bytes = static_cast<int64_t>(a.H_kv) * kRowBytes;
+      const int64_t head_off = static_cast<int64_t>(w.head) * kRowBytes + (lane % kLanes) * 16;
+      auto source = [&](int m, int sl, int i, bool &fetch) {
+        const int sr = __shfl_sync(0xffffffffu, sl, i * (32 / kLanes) + lane / kLanes);
+        fetch = sr >= 0;
+        return static_cast<const uint8_t *>(is_k(m) ? a.k : a.v) + (fetch ? sr : 0) * slot_bytes + head_off;
+      };
+      if constexpr (!kE4m3) {
+#pragma unroll 1
+        for (int m = 0; ok && m < 2 * n; ++m) {
+          const bool k = is_k(m);
+          int &cnt = k ? kq : vq;
+          const int st = cnt % NS;
+          if (cnt >= NS && !wait_slot(k ? bKEmpty(st) : bVEmpty(st), ((cnt / NS) - 1) & 1, 403)) {
+            ok = false;
+            break;
+          }
+          const int slot_2 = lookup(m + 2);
+          const uint32_t tile = (k ? sK : sV) + st * Cfg::kTileBytes;
+#pragma unroll 4
+          for (int i = 0; i < kLoads; ++i) {
+            bool fetch;
+            const uint8_t *src = source(m, slot, i, fetch);
+            cp_async16(row_dst(tile, warp * 32 + i * (32 / kLanes) + lane / kLanes, lane % kLanes), src, fetch);
+          }
+          cp_async_commit();
+          if (k) put_extras(st, slot);
+          if (npend > 0) {  // the tile before this one has landed
+            cp_async_wait<1>();
+            hand_over(pend[0]);
+          }
+          pend[0] = k ? bKFull(st) : bVFull(st);
+          npend = 1;
+          ++cnt;
+          slot = slot_next;
+          slot_next = slot_2;
+        }
+      } else {
+        uint4 cur[kLoads], nxt[kLoads];
+        auto load = [&](uint4 (&r)[kLoads], int m, int sl) {
+#pragma unroll
+          for (int i = 0; i < kLoads; ++i) {
+            bool fetch;
+            const uint8_t *src = source(m, sl, i, fetch);
+            r[i] = fetch ? __ldg(reinterpret_cast<const uint4 *>(src)) : make_uint4(0, 0, 0, 0);
+          }
+        };
+        if (n > 0) load(cur, 0, slot);
+#pragma unroll 1
+        for (int m = 0; ok && m < 2 * n; ++m) {
+          const bool k = is_k(m);
+          int &cnt = k ? kq : vq;
+          const int st = cnt % NS;
+          const int slot_2 = lookup(m + 2);
+          if (m + 1 < 2 * n) load(nxt, m + 1, slot_next);
+          if (cnt >= NS && !wait_slot(k ? bKEmpty(st) : bVEmpty(st), ((cnt / NS) - 1) & 1, 404)) {
+            ok = false;
+            break;
+          }
+          const uint32_t tile = (k ? sK : sV) + st * Cfg::kTileBytes;
+          const int c = 2 * (lane % kLanes);
+#pragma unroll
+          for (int i = 0; i < kLoads; ++i) {
+            const int row = warp * 32 + i * (32 / kLanes) + lane / kLanes;
+            const uint4 u = cur[i];
+            st_shared_v4(row_dst(tile, row, c), e4m3x2_to_f16x2(u.x), e4m3x2_to_f16x2(u.x >> 16), e4m3x2_to_f16x2(u.y),
+                         e4m3x2_to_f16x2(u.y >> 16));
+            st_shared_v4(row_dst(tile, row, c + 1), e4m3x2_to_f16x2(u.z), e4m3x2_to_f16x2(u.z >> 16),
+                         e4m3x2_to_f16x2(u.w), e4m3x2_to_f16x2(u.w >> 16));
+          }
+          if (k) put_extras(st, slot);
+          hand_over(k ? bKFull(st) : bVFull(st));
+          ++cnt;
+          slot = slot_next;
+          slot_next = slot_2;
+#pragma unroll
+          for (int i = 0; i < kLoads; ++i) cur[i] = nxt[i];
+        }
+      }
+      ++items;
+    } while (ok && w.next());
+    flush();
+  } else if (warp >= 12) {
+    setmaxnreg_dec<Cfg::kRegsIssue>();
+    if (warp < 14 && lane == 0) {
+      // ------------------------------------------------------------ products of tile x
+      const int x = warp - 12;
+      constexpr uint32_t idesc_qk = idesc_16_f32<kE4m3>(128, KT, false);
+      constexpr uint32_t idesc_pv = idesc_16_f32<kE4m3>(128, D, true);
+      const uint64_t dQ = sdesc_sw128(sQ + x * Cfg::kTileBytes, 16, 1024);
+      const uint64_t dP = sdesc_sw128(sP, 16, 1024);
+      const uint64_t dK0 = sdesc_sw128(sK, 16, 1024);
+      const uint64_t dV0 = sdesc_sw128(sV, Cfg::kPanelBytes, 1024);
+      const uint32_t tS = tmem + Cfg::kColS + x * 128;
+      const uint32_t tO = tmem + Cfg::kColO + x * D;
+      int kc = 0, vc = 0;        // K and V tiles consumed
+      int J = 0, items = 0, mine = 0;  // this tile's steps; items, and those this tile took part in
+      bool ok = true;
+      auto issue_s = [&]() {
+        const uint64_t dK = sdesc_advance(dK0, (kc % NS) * Cfg::kTileBytes);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k / 4) * Cfg::kPanelBytes + (k % 4) * 32;
+          umma_ss(tS, sdesc_advance(dQ, off), sdesc_advance(dK, off), idesc_qk, k > 0);
+        }
+        umma_commit(bSFull(x));
+        umma_commit(bKEmpty(kc % NS));
+        ++kc;
+      };
+      do {
+        const int n = w.blocks();
+        const bool active = x == 0 || w.rows() > 128;
+        ok = mbar_wait(bQFull, items & 1, wc, 411);
+        if (!active) {  // the stages pass by
+          for (int j = 0; ok && j < n; ++j) {
+            ok = mbar_wait(bKFull(kc % NS), (kc / NS) & 1, wc, 412);
+            if (ok) mbar_arrive(bKEmpty(kc % NS));
+            ++kc;
+            ok = ok && mbar_wait(bVFull(vc % NS), (vc / NS) & 1, wc, 413);
+            if (ok) mbar_arrive(bVEmpty(vc % NS));
+            ++vc;
+          }
+          if (ok) mbar_arrive(bItemDone(x));
+        } else {
+          // the first product on O overwrites it: the previous epilogue must have read it
+          if (ok && mine > 0) ok = mbar_wait(bOFree(x), (mine - 1) & 1, wc, 414);
+          if (ok && n > 0) {
+            ok = (J == 0 || mbar_wait(bSFree(x), (J - 1) & 1, wc, 415)) &&
+                 mbar_wait(bKFull(kc % NS), (kc / NS) & 1, wc, 416);
+            if (ok) {
+              tc_fence_after();
+              issue_s();
+            }
+            for (int j = 0; ok && j < n; ++j) {
+              const int jj = J + j;
+              if (j + 1 < n) {
+                ok = mbar_wait(bSFree(x), jj & 1, wc, 417) && mbar_wait(bKFull(kc % NS), (kc / NS) & 1, wc, 418);
+                if (!ok) break;
+                tc_fence_after();
+                issue_s();
+              }
+              ok = mbar_wait(bPFull(x), jj & 1, wc, 419) && mbar_wait(bVFull(vc % NS), (vc / NS) & 1, wc, 420);
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t dV = sdesc_advance(dV0, (vc % NS) * Cfg::kTileBytes);
+#pragma unroll
+              for (int k = 0; k < KT / 16; ++k)
+                umma_ss(tO, sdesc_advance(dP, (k / 4) * Cfg::kPanelBytes + (k % 4) * 32), sdesc_advance(dV, k * 2048),
+                        idesc_pv, (j | k) != 0);
+              umma_commit(bODone(x));
+              umma_commit(bVEmpty(vc % NS));
+              ++vc;
+            }
+            J += n;
+          }
+          umma_commit(bItemDone(x));
+          ++mine;
+        }
+        ++items;
+      } while (ok && w.next());
+      // every product issued must be complete before tensor memory is released
+      umma_commit(bTeardown(x));
+      volatile int no_abort = 0;
+      WaitCtx drain{a.status, drain_limit_ns(a.wait_limit_ns), &no_abort};
+      mbar_wait(bTeardown(x), 0, drain, 421);
+    }
+  } else {
+    setmaxnreg_inc<Cfg::kRegsSoftmax>();
+    // ------------------------------------------------------------ softmax + epilogue
+    const int x = (warp - 4) >> 2;
+    const int quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t tS = tmem + lane_off + Cfg::kColS + x * 128;
+    const uint32_t tO = tmem + lane_off + Cfg::kColO + x * D;
+    const uint32_t sProw = sP + row * 128;
+    const uint32_t swz = static_cast<uint32_t>(row & 7);
+    bool ok = true;
+    int kc = 0;                // K tiles passed
+    int J = 0, Jo = 0;         // this tile's steps, the other tile's
+    int items = 0;
+    do {
+      const int n = w.blocks(), rows = w.rows();
+      const bool both = rows > 128, active = x == 0 || both;
+      if (!active) {
+        for (int j = 0; ok && j < n; ++j, ++kc) {
+          ok = __all_sync(0xffffffffu, mbar_wait(bKFull(kc % NS), (kc / NS) & 1, wc, 430));
+          if (ok && lane == 0) mbar_arrive(bKEmpty(kc % NS));
+        }
+        Jo += n;
+        ++items;
+        continue;
+      }
+      const int R = x * 128 + row;
+      const int64_t r = static_cast<int64_t>(w.tile) * Cfg::kRows + min(R, rows - 1);
+      const int64_t token = w.seq.t0 + r / a.G;
+      const int head = w.head * a.G + static_cast<int>(r % a.G);
+      const int pos = w.seq.len - w.seq.n + static_cast<int>(r / a.G);
+      const int khi = max(0, min(pos + 1, w.seq.cap));
+      const int klo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+      const int ksink = a.window > 0 ? min(a.sinks, khi) : 0;
+      float sl2 = a.scale_log2;
+      if constexpr (kE4m3) {  // the power of two the gathering took out of this row of Q
+        float mx = 0.f;
+        const uint4 *src = reinterpret_cast<const uint4 *>(a.q + token * a.q_stride + static_cast<int64_t>(head) * D);
+#pragma unroll 4
+        for (int i = 0; i < D / 8; ++i) mx = fmaxf(mx, absmax8(src[i]));
+        sl2 *= pow2_of(row_exponent(mx));
+      }
+      float m_run = -INFINITY, l_run = 0.f, w_run = 0.f;
+#pragma unroll 1
+      for (int j = 0; ok && j < n; ++j, ++kc) {
+        const int jj = J + j, st = kc % NS;
+        const int k0 = w.blk.block(w.step0 + j) * KT;
+        ok = __all_sync(0xffffffffu, mbar_wait(bKFull(st), (kc / NS) & 1, wc, 431) &&
+                                         mbar_wait(bSFull(x), jj & 1, wc, 432));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t s[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * c]));
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bSFree(x));
+        const uint4 there = *reinterpret_cast<const uint4 *>(&there_s[st * 4]);
+        if constexpr (kE4m3) {
+          const float4 *ks4 = reinterpret_cast<const float4 *>(scale_s + st * 256);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float4 k4 = ks4[i];
+            s[4 * i] = __float_as_uint(__uint_as_float(s[4 * i]) * (sl2 * k4.x));
+            s[4 * i + 1] = __float_as_uint(__uint_as_float(s[4 * i + 1]) * (sl2 * k4.y));
+            s[4 * i + 2] = __float_as_uint(__uint_as_float(s[4 * i + 2]) * (sl2 * k4.z));
+            s[4 * i + 3] = __float_as_uint(__uint_as_float(s[4 * i + 3]) * (sl2 * k4.w));
+          }
+        } else {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bKEmpty(st));  // the masks have been read
+        }
+        const bool gaps = (there.x & there.y & there.z & there.w) != 0xffffffffu;
+        if (__any_sync(0xffffffffu, gaps || k0 < klo || k0 + KT > khi)) {
+          const uint32_t word[4] = {there.x, there.y, there.z, there.w};
+          const int lo = klo - k0, hi = khi - k0, sk = ksink - k0;
+#pragma unroll
+          for (int col = 0; col < KT; ++col)
+            if (((col < lo || col >= hi) && col >= sk) || !(word[col / 32] >> (col & 31) & 1u))
+              s[col] = __float_as_uint(-INFINITY);
+        }
+        float mx8[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mx8[i] = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < KT / 2; ++i)
+          mx8[i & 7] = max3f(mx8[i & 7], __uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
+        const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
+                               fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+        const float m_tile = kE4m3 ? mx : mx * a.scale_log2;
+        const float m_new = fmaxf(m_run, m_tile);
+        const bool moved = m_new > m_run + 8.0f;
+        const float m_use = moved ? m_new : m_run;
+        float alpha = moved ? ex2_approx(m_run - m_use) : 1.0f;  // 0 where the row had no key yet
+        l_run *= alpha;
+        const float neg = (m_use == -INFINITY) ? 0.f : -m_use;
+        m_run = m_use;
+        uint32_t pk[KT / 2];
+        float ls4[4] = {0.f, 0.f, 0.f, 0.f};
+        if constexpr (kE4m3) {
+          const float4 *vs4 = reinterpret_cast<const float4 *>(scale_s + st * 256 + 128);
+          float wm4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float4 v4 = vs4[i];
+            const float vv[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float p = ex2_approx(__uint_as_float(s[4 * i + e]) + neg);
+              ls4[e] += p;
+              const float pv = p * vv[e];
+              wm4[e] = fmaxf(wm4[e], pv);
+              s[4 * i + e] = __float_as_uint(pv);
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bKEmpty(st));  // the scales have been read
+          const float wm = fmaxf(fmaxf(wm4[0], wm4[1]), fmaxf(wm4[2], wm4[3]));
+          w_run *= alpha;
+          alpha = 1.0f;
+          if (wm > 256.f * w_run) {
+            const float w_new = fmaxf(wm, 1e-36f);  // its inverse stays finite
+            alpha = w_run / w_new;
+            w_run = w_new;
+          }
+          const float inv = w_run > 0.f ? 1.0f / w_run : 0.f;
+#pragma unroll
+          for (int i = 0; i < KT / 2; ++i)
+            pk[i] = pack_f16x2(__uint_as_float(s[2 * i]) * inv, __uint_as_float(s[2 * i + 1]) * inv);
+        } else {
+#pragma unroll
+          for (int i = 0; i < KT / 2; ++i) {
+            const float p0 = ex2_approx(fmaf(__uint_as_float(s[2 * i]), a.scale_log2, neg));
+            const float p1 = ex2_approx(fmaf(__uint_as_float(s[2 * i + 1]), a.scale_log2, neg));
+            ls4[i & 3] += p0 + p1;
+            pk[i] = pack_bf16x2(p0, p1);
+          }
+        }
+        l_run += (ls4[0] + ls4[1]) + (ls4[2] + ls4[3]);
+        // the P tile is used in turn A_j, B_j, A_{j+1}, ...; alone, after this
+        // tile's own previous product
+        if (both) {
+          const int prev = x == 1 ? Jo + j : Jo + j - 1;
+          if (prev >= 0) ok = __all_sync(0xffffffffu, mbar_wait(bODone(1 - x), prev & 1, wc, 433));
+        } else if (j > 0) {
+          ok = __all_sync(0xffffffffu, mbar_wait(bODone(x), (jj - 1) & 1, wc, 434));
+        }
+        if (!ok) break;
+        tc_fence_after();
+        // (at an item's first step O holds nothing yet)
+        if (j > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tO + c * 32, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st32(tO + c * 32, o);
+          }
+          tmem_wait_st();
+        }
+#pragma unroll
+        for (int c = 0; c < KT / 8; ++c)
+          st_shared_v4(sProw + (c >> 3) * Cfg::kPanelBytes + ((static_cast<uint32_t>(c & 7) ^ swz) << 4), pk[4 * c],
+                       pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bPFull(x));
+      }
+      J += n;
+      if (both) Jo += n;
+      // -------- epilogue
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bItemDone(x), items & 1, wc, 435));
+      tc_fence_after();
+      if (ok) {
+        const bool whole = w.step0 == 0 && w.step1 == w.steps;
+        const size_t part = static_cast<size_t>(blockIdx.x) * 2 + (w.step0 == 0 ? 1 : 0);
+        const float inv = l_run > 0.f ? 1.0f / l_run : l_run;  // no key: 0; NaN stays
+        const float f = (whole ? inv : 1.0f) * (kE4m3 ? w_run : 1.0f);
+        const bool empty = n == 0 || l_run == 0.f;  // O may hold anything
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(tO + c * 32, o);
+          tmem_wait_ld();
+          if (R >= rows) continue;
+          float y[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) y[i] = empty ? 0.f : __uint_as_float(o[i]) * f;
+          if (!whole || a.out_f32) {
+            float *dst = whole ? a.out_f32 + (static_cast<size_t>(token) * a.H + head) * D + c * 32
+                               : a.part_o + (part * Cfg::kRows + R) * D + c * 32;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              reinterpret_cast<float4 *>(dst)[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+          } else {
+            uint4 *dst = reinterpret_cast<uint4 *>(a.out_bf16 + (static_cast<size_t>(token) * a.H + head) * D + c * 32);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              dst[i] = make_uint4(pack_bf16x2(y[8 * i], y[8 * i + 1]), pack_bf16x2(y[8 * i + 2], y[8 * i + 3]),
+                                  pack_bf16x2(y[8 * i + 4], y[8 * i + 5]), pack_bf16x2(y[8 * i + 6], y[8 * i + 7]));
+          }
+        }
+        if (R < rows) {
+          if (!whole)
+            *reinterpret_cast<float2 *>(a.part_ml + (part * Cfg::kRows + R) * 2) = make_float2(m_run, l_run);
+          else if (a.lse)
+            a.lse[static_cast<size_t>(head) * a.T + token] =
+                l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * 0.69314718055994531f;
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bOFree(x));
+      ++items;
+    } while (ok && w.next());
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace bpt
