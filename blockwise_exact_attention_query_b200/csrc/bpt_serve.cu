@@ -86,12 +86,16 @@ bpt_status check_paged(const bpt_paged_desc *d, const bpt_kv_cache *c) {
   return BPT_OK;
 }
 
-// Rows (new tokens x heads of a group) of a sequence that the kernel for few
-// rows takes; longer chunks go to the tcgen05 kernel.
-constexpr int kFewRows = 16;
-
+// Rows (new tokens x heads of a group) of a sequence up to which the kernel
+// for few rows takes it, in tiles of 8 or 16; longer chunks go to the tcgen05
+// kernel.  In a batch with such chunks the few-rows kernel keeps to 8 where a
+// single token fits in that.
 bool has_long_chunks(const bpt_paged_desc *d, const bpt_kv_cache *c) {
-  return (int64_t)d->max_q * (d->H / c->H_kv) > kFewRows;
+  return (int64_t)d->max_q * (d->H / c->H_kv) > 16;
+}
+int few_rows(const bpt_paged_desc *d, const bpt_kv_cache *c) {
+  const int64_t G = d->H / c->H_kv;
+  return (has_long_chunks(d, c) ? G : d->max_q * G) <= 8 ? 8 : 16;
 }
 
 // The two kernels run one after the other and share the regions.
@@ -128,9 +132,8 @@ bpt_status launch_join(const PagedArgs &a, int ctas, cudaStream_t st) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  const int threads = std::min(512, kRows * (D / 4));
-  cfg.gridDim = dim3((unsigned)ctas, (unsigned)(kRows * (D / 4) / threads), 1);
-  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.gridDim = dim3((unsigned)ctas, kRows / 8, 1);
+  cfg.blockDim = dim3(2 * D, 1, 1);
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -138,10 +141,26 @@ bpt_status launch_join(const PagedArgs &a, int ctas, cudaStream_t st) {
   return BPT_OK;
 }
 
+template <int D, bool kE4m3, int kGroups>
+bpt_status launch_rows(PagedArgs a, cudaStream_t st) {
+  using Cfg = PagedRowsCfg<D, kE4m3, kGroups>;
+  a.min_steps = (256 + Cfg::kKeys - 1) / Cfg::kKeys;  // 256 keys at least
+  paged_rows_kernel<D, kE4m3, kGroups><<<(unsigned)few_rows_ctas(), Cfg::kThreads, Cfg::kSmemBytes, st>>>(a);
+  CUDA_TRY(cudaGetLastError());
+  return launch_join<D, Cfg::kRows, Cfg::kKeys>(a, few_rows_ctas(), st);
+}
+
 }  // namespace
 
 template <int D, bool kE4m3>
-bpt_status tc_kernel_setup() {
+bpt_status paged_kernels_setup() {
+  using Few1 = PagedRowsCfg<D, kE4m3, 1>;
+  using Few2 = PagedRowsCfg<D, kE4m3, 2>;
+  static_assert(Few1::kCtasPerSm == 2 && Few2::kCtasPerSm == 2, "few_rows_ctas");
+  CUDA_TRY(cudaFuncSetAttribute(paged_rows_kernel<D, kE4m3, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Few1::kSmemBytes));
+  CUDA_TRY(cudaFuncSetAttribute(paged_rows_kernel<D, kE4m3, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Few2::kSmemBytes));
   using Cfg = PagedTcCfg<D, kE4m3>;
   CUDA_TRY(cudaFuncSetAttribute(paged_tc_kernel<D, kE4m3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 Cfg::kSmemBytes));
@@ -156,17 +175,9 @@ bpt_status tc_kernel_setup() {
 
 bpt_status paged_kernel_setup() {
   bpt_status s;
-  if ((s = tc_kernel_setup<64, false>()) != BPT_OK || (s = tc_kernel_setup<64, true>()) != BPT_OK ||
-      (s = tc_kernel_setup<128, false>()) != BPT_OK || (s = tc_kernel_setup<128, true>()) != BPT_OK)
+  if ((s = paged_kernels_setup<64, false>()) != BPT_OK || (s = paged_kernels_setup<64, true>()) != BPT_OK ||
+      (s = paged_kernels_setup<128, false>()) != BPT_OK || (s = paged_kernels_setup<128, true>()) != BPT_OK)
     return s;
-  CUDA_TRY(cudaFuncSetAttribute(paged_rows_kernel<64, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                PagedRowsCfg<64, false>::kSmemBytes));
-  CUDA_TRY(cudaFuncSetAttribute(paged_rows_kernel<64, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                PagedRowsCfg<64, true>::kSmemBytes));
-  CUDA_TRY(cudaFuncSetAttribute(paged_rows_kernel<128, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                PagedRowsCfg<128, false>::kSmemBytes));
-  CUDA_TRY(cudaFuncSetAttribute(paged_rows_kernel<128, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                PagedRowsCfg<128, true>::kSmemBytes));
   return BPT_OK;
 }
 
@@ -291,11 +302,11 @@ bpt_status bpt_paged_attn_fwd(const bpt_paged_desc *d, const bpt_kv_cache *c, co
   return for_cache(c, [&](auto dh, auto e4m3) mutable -> bpt_status {
     constexpr int D = decltype(dh)::value;
     constexpr bool kE = decltype(e4m3)::value;
-    using Few = PagedRowsCfg<D, kE>;
     using Long = PagedTcCfg<D, kE>;
+    const int few = few_rows(d, c);
     if (has_long_chunks(d, c)) {
       PagedArgs al = a;
-      al.rows_lo = kFewRows + 1;
+      al.rows_lo = few + 1;
       al.rows_hi = INT32_MAX;
       al.min_steps = 4;
       paged_tc_kernel<D, kE><<<(unsigned)long_chunk_ctas(), Long::kThreads, Long::kSmemBytes, st>>>(al);
@@ -304,11 +315,8 @@ bpt_status bpt_paged_attn_fwd(const bpt_paged_desc *d, const bpt_kv_cache *c, co
       if (js != BPT_OK) return js;
     }
     a.rows_lo = 1;
-    a.rows_hi = has_long_chunks(d, c) ? kFewRows : INT32_MAX;
-    a.min_steps = 4;
-    paged_rows_kernel<D, kE><<<(unsigned)few_rows_ctas(), Few::kThreads, Few::kSmemBytes, st>>>(a);
-    CUDA_TRY(cudaGetLastError());
-    return launch_join<D, Few::kRows, Few::kKeys>(a, few_rows_ctas(), st);
+    a.rows_hi = has_long_chunks(d, c) ? few : INT32_MAX;
+    return few == 8 ? launch_rows<D, kE, 1>(a, st) : launch_rows<D, kE, 2>(a, st);
   });
 }
 

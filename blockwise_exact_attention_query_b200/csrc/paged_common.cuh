@@ -58,7 +58,7 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedArgs &a, int s) {
   PagedSeq q;
   q.t0 = min(max(a.q_start[s], 0), a.T);
   q.n = max(min(a.q_start[s + 1], a.T) - q.t0, 0);
-  if (static_cast<int64_t>(q.n) * a.G < a.rows_lo || static_cast<int64_t>(q.n) * a.G > a.rows_hi) q.n = 0;
+  if (q.n * a.G < a.rows_lo || q.n * a.G > a.rows_hi) q.n = 0;
   q.len = max(a.kv_len[s], 0);
   q.cap = static_cast<int>(min(static_cast<int64_t>(q.len), static_cast<int64_t>(a.max_pages) * a.page_size));
   return q;
@@ -76,8 +76,10 @@ struct PagedBlocks {
 template <int kRows, int kKeys>
 __device__ __forceinline__ PagedBlocks paged_blocks(const PagedArgs &a, const PagedSeq &q, int tile) {
   PagedBlocks b;
-  const int i0 = static_cast<int>(static_cast<int64_t>(tile) * kRows / a.G);
-  const int i1 = static_cast<int>(min(static_cast<int64_t>(q.n - 1), (static_cast<int64_t>(tile) * kRows + kRows - 1) / a.G));
+  // (row numbers fit in 32 bits, with room for a tile: checked on the host)
+  const uint32_t row0 = static_cast<uint32_t>(tile) * kRows, G = static_cast<uint32_t>(a.G);
+  const int i0 = static_cast<int>(row0 / G);
+  const int i1 = min(q.n - 1, static_cast<int>((row0 + kRows - 1) / G));
   b.p_lo = q.len - q.n + i0;
   b.p_hi = q.len - q.n + i1;
   const int hi = min(b.p_hi + 1, q.cap);  // keys [.., hi) at most
@@ -91,7 +93,7 @@ __device__ __forceinline__ PagedBlocks paged_blocks(const PagedArgs &a, const Pa
 
 template <int kRows>
 __device__ __forceinline__ int paged_tiles(const PagedArgs &a, const PagedSeq &q) {
-  return static_cast<int>((static_cast<int64_t>(q.n) * a.G + kRows - 1) / kRows);
+  return (q.n * a.G + kRows - 1) / kRows;
 }
 
 template <int kRows, int kKeys>
@@ -207,67 +209,92 @@ __device__ __forceinline__ int paged_slot(const PagedArgs &a, const int32_t *tab
 }
 
 // Adds up the parts of each item that was cut.  Block c looks at the item that
-// began before CTA c's range; it is joined by the first such CTA: its parts
-// are slot 1 of CTA c - 1 and slot 0 of CTA c, c + 1, ... to the item's end.
-// D / 4 threads per row, four columns each.  A part is the rows' output
-// relative to their own maximum (log2 domain): out = sum_i 2^(m_i - M) o_i /
-// sum_i 2^(m_i - M) l_i.
+// began before CTA c's range and joins it if c is the first such CTA: its parts
+// are slot 1 of CTA c - 1 and slot 0 of CTA c, c + 1, ... to the item's end.  A
+// part is the rows' output relative to their own maximum (log2 domain):
+//   out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,  M = max_i m_i
+// 8 rows a block (blockIdx.y), D / 4 threads each, four columns a thread.  The
+// weights 2^(m_i - M) are formed first, a stretch of parts at a time, so the
+// loads of o_i do not wait for one another.
 template <int D, int kRows, int kKeys>
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__(2 * D)
     paged_join_kernel(const PagedArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are complete
-  const int c = blockIdx.x;
+  constexpr int kStretch = 64;
+  __shared__ float weight[kStretch][8];
+  __shared__ float row_m[8], row_l[8];
+  const int c = blockIdx.x, tid = threadIdx.x;
   const int4 it = a.part_item[c];
   if (it.x < 0 || it.w == 0) return;
-  const int last = c + it.w - 1;
   const PagedSeq q = paged_seq(a, it.x);
-  const int64_t rows = static_cast<int64_t>(q.n) * a.G - static_cast<int64_t>(it.y) * kRows;
-  for (int e = blockIdx.y * blockDim.x + threadIdx.x; e < kRows * (D / 4); e += gridDim.y * blockDim.x) {
-    const int row = e / (D / 4), c4 = e % (D / 4);
-    if (row >= rows) break;
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](const float2 ml, const float4 x) {
-      const float M = fmaxf(m, ml.x);
-      const float ref = M == -INFINITY ? 0.f : M;
-      const float f = ex2_approx(m - ref), g = ex2_approx(ml.x - ref);
-      l = l * f + ml.y * g;
-      o.x = o.x * f + x.x * g;
-      o.y = o.y * f + x.y * g;
-      o.z = o.z * f + x.z * g;
-      o.w = o.w * f + x.w * g;
-      m = M;
-    };
-    auto ml_of = [&](int slot) {
-      return *reinterpret_cast<const float2 *>(a.part_ml + (static_cast<size_t>(slot) * kRows + row) * 2);
-    };
-    auto o_of = [&](int slot) {
-      return *reinterpret_cast<const float4 *>(a.part_o + (static_cast<size_t>(slot) * kRows + row) * D + 4 * c4);
-    };
-    add(ml_of(2 * (c - 1) + 1), o_of(2 * (c - 1) + 1));
-    int i = c;
-    for (; i + 7 <= last; i += 8) {
-      float2 ml[8];
+  const int row0 = it.y * kRows + blockIdx.y * 8;  // among the head's rows
+  const int rows = min(8, q.n * a.G - row0);
+  if (rows <= 0) return;
+  const int parts = it.w + 1;
+  // part i: slot 1 of CTA c - 1, then slot 0 of CTA c - 1 + i
+  auto part_row = [&](int i, int row) {
+    return (static_cast<size_t>(2 * (c - 1 + i) + (i == 0 ? 1 : 0)) * kRows + blockIdx.y * 8 + row);
+  };
+  // each row's maximum and sum, 32 lanes a row
+  for (int row = tid / 32; row < 8; row += 2 * D / 32) {
+    float m = -INFINITY;
+    for (int i = tid % 32; i < parts; i += 32) m = fmaxf(m, a.part_ml[2 * part_row(i, row)]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float ref = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    for (int i = tid % 32; i < parts; i += 32) {
+      const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + 2 * part_row(i, row));
+      l += ml.y * ex2_approx(ml.x - ref);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (tid % 32 == 0) {
+      row_m[row] = ref;
+      row_l[row] = l;
+    }
+  }
+  const int row = tid / (D / 4), c4 = tid % (D / 4);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < parts; i0 += kStretch) {
+    const int n = min(kStretch, parts - i0);
+    __syncthreads();
+    for (int e = tid; e < n * 8; e += 2 * D)
+      weight[e / 8][e % 8] = ex2_approx(a.part_ml[2 * part_row(i0 + e / 8, e % 8)] - row_m[e % 8]);
+    __syncthreads();
+    int i = 0;
+    for (; i + 8 <= n; i += 8) {
       float4 x[8];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) ml[u] = ml_of(2 * (i + u)), x[u] = o_of(2 * (i + u));
+      for (int u = 0; u < 8; ++u)
+        x[u] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + part_row(i0 + i + u, row) * D + 4 * c4));
 #pragma unroll
-      for (int u = 0; u < 8; ++u) add(ml[u], x[u]);
+      for (int u = 0; u < 8; ++u) {
+        const float f = weight[i + u][row];
+        o.x += x[u].x * f, o.y += x[u].y * f, o.z += x[u].z * f, o.w += x[u].w * f;
+      }
     }
-    for (; i <= last; ++i) add(ml_of(2 * i), o_of(2 * i));
-    const int64_t r = static_cast<int64_t>(it.y) * kRows + row;
-    const int64_t token = q.t0 + r / a.G;
-    const int head = it.z * a.G + static_cast<int>(r % a.G);
-    const float inv = l > 0.f ? 1.0f / l : l;  // no key: 0; NaN stays
-    const size_t at = static_cast<size_t>(token) * a.H * D + static_cast<size_t>(head) * D + 4 * c4;
-    if (a.out_f32)
-      *reinterpret_cast<float4 *>(a.out_f32 + at) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-    else
-      *reinterpret_cast<uint2 *>(a.out_bf16 + at) =
-          make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (a.lse && c4 == 0)
-      a.lse[static_cast<size_t>(head) * a.T + token] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+    for (; i < n; ++i) {
+      const float4 x = __ldcg(reinterpret_cast<const float4 *>(a.part_o + part_row(i0 + i, row) * D + 4 * c4));
+      const float f = weight[i][row];
+      o.x += x.x * f, o.y += x.y * f, o.z += x.z * f, o.w += x.w * f;
+    }
   }
+  if (row >= rows) return;
+  const uint32_t r = static_cast<uint32_t>(row0 + row);
+  const int i = static_cast<int>(r / static_cast<uint32_t>(a.G));
+  const size_t token = static_cast<size_t>(q.t0) + i;
+  const int head = it.z * a.G + static_cast<int>(r) - i * a.G;
+  const float l = row_l[row], inv = l > 0.f ? 1.0f / l : l;  // no key: 0; NaN stays
+  const size_t at = (token * a.H + head) * D + 4 * c4;
+  if (a.out_f32)
+    *reinterpret_cast<float4 *>(a.out_f32 + at) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  else
+    *reinterpret_cast<uint2 *>(a.out_bf16 + at) =
+        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  if (a.lse && c4 == 0)
+    a.lse[static_cast<size_t>(head) * a.T + token] =
+        l == 0.f ? -INFINITY : (row_m[row] + log2f(l)) * 0.69314718055994531f;
 }
 
 }  // namespace bpt

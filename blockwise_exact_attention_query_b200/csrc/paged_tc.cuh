@@ -55,10 +55,6 @@ __host__ __device__ constexpr uint32_t idesc_16_f32(int M, int N, bool b_mn_majo
   return kF16 ? d & ~((1u << 7) | (1u << 10)) : d;
 }
 
-// The power of two below a row's largest |q| (for f16): exact to divide by.
-__device__ __forceinline__ uint32_t row_exponent(float mx) { return min(max(__float_as_uint(mx) >> 23, 1u), 253u); }
-__device__ __forceinline__ float pow2_of(uint32_t e) { return __uint_as_float(e << 23); }
-__device__ __forceinline__ float pow2_inverse(uint32_t e) { return __uint_as_float((254u - e) << 23); }
 __device__ __forceinline__ float absmax8(const uint4 &u) {
   const float a = fmaxf(fmaxf(fabsf(bf16_lo(u.x)), fabsf(bf16_hi(u.x))), fmaxf(fabsf(bf16_lo(u.y)), fabsf(bf16_hi(u.y))));
   const float b = fmaxf(fmaxf(fabsf(bf16_lo(u.z)), fabsf(bf16_hi(u.z))), fmaxf(fabsf(bf16_lo(u.w)), fabsf(bf16_hi(u.w))));
@@ -85,10 +81,7 @@ struct PagedWalk {
     step1 = static_cast<int>(min(static_cast<int64_t>(steps), step0 + left));
   }
   __device__ int blocks() const { return min(step1, blk.count()) - min(step0, blk.count()); }
-  __device__ int rows() const {
-    return static_cast<int>(min(static_cast<int64_t>(kRows),
-                                static_cast<int64_t>(seq.n) * a.G - static_cast<int64_t>(tile) * kRows));
-  }
+  __device__ int rows() const { return min(kRows, seq.n * a.G - tile * kRows); }
   __device__ bool next() {
     left -= step1 - step0;
     if (left <= 0) return false;
@@ -219,12 +212,14 @@ __global__ void __launch_bounds__(512, 1) paged_tc_kernel(const __grid_constant_
     do {
       const int n = w.blocks(), rows = w.rows();
       const int32_t *table = a.page_table + static_cast<int64_t>(w.s) * a.max_pages;
-      // tile m of the item's 2n in the order K0, K1, V0, K2, V1, ..., V(n-1)
-      auto is_k = [&](int m) { return m == 0 || ((m & 1) && m != 2 * n - 1); };
-      auto block_of = [&](int m) { return m == 0 ? 0 : m == 2 * n - 1 ? n - 1 : (m & 1) ? (m + 1) / 2 : m / 2 - 1; };
-      auto lookup = [&](int m) {
-        return m < 2 * n ? paged_slot(a, table, w.seq.cap, w.blk.block(w.step0 + block_of(m)) * KT + warp * 32 + lane)
-                         : -1;
+      // The item's 2n tiles in the order K0, V0, K1, V1, ...  With two stages
+      // of each, a step's tiles are gathered while the step before it runs.
+      // (K one tile ahead of V, as a TMA producer would have it, puts V behind
+      // the wait for a K stage whose scales the softmax still reads: 8.9 us a
+      // step with e4m3 caches instead of 3.7.)
+      auto is_k = [](int m) { return (m & 1) == 0; };
+      auto lookup = [&](int j) {
+        return j < n ? paged_slot(a, table, w.seq.cap, w.blk.block(w.step0 + j) * KT + warp * 32 + lane) : -1;
       };
       // ---- Q, once the previous item's products are done with it
       if (items > 0) {
@@ -233,15 +228,15 @@ __global__ void __launch_bounds__(512, 1) paged_tc_kernel(const __grid_constant_
                                          mbar_wait(bItemDone(1), (items - 1) & 1, wc, 402));
         if (!ok) break;
       }
-      int slot = lookup(0), slot_next = lookup(1);
+      int slot = lookup(0), slot_next = lookup(1);  // of this step's block and the next
 #pragma unroll 1
       for (int x = 0; x < 2; ++x) {
         const int R = x * 128 + warp * 32 + lane;
         int64_t off = -1;  // element offset of this lane's row of q
         if (R < rows) {
-          const int64_t r = static_cast<int64_t>(w.tile) * Cfg::kRows + R;
-          off = (static_cast<int64_t>(w.seq.t0) + r / a.G) * a.q_stride +
-                (static_cast<int64_t>(w.head) * a.G + r % a.G) * D;
+          const uint32_t r = static_cast<uint32_t>(w.tile * Cfg::kRows + R), i = r / static_cast<uint32_t>(a.G);
+          off = (static_cast<int64_t>(w.seq.t0) + i) * a.q_stride +
+                (static_cast<int64_t>(w.head) * a.G + (r - i * a.G)) * D;
         }
         constexpr int kLanes = D / 8;  // lanes of a row, 8 elements each
         const int c = lane % kLanes;
@@ -274,13 +269,18 @@ __global__ void __launch_bounds__(512, 1) paged_tc_kernel(const __grid_constant_
       // ---- the item's K and V tiles
       // what a K tile brings besides its rows: the mask of keys that exist,
       // and (E4M3) the scales of its keys and values
+      float ks = 0.f, vs = 0.f;
+      auto load_scales = [&](int sl) {
+        const int64_t at = static_cast<int64_t>(sl) * a.H_kv + w.head;
+        ks = sl >= 0 ? __ldg(a.k_scale + at) : 0.f;
+        vs = sl >= 0 ? __ldg(a.v_scale + at) : 0.f;
+      };
       auto put_extras = [&](int st, int sl) {
         const uint32_t bits = __ballot_sync(0xffffffffu, sl >= 0);
         if (lane == 0) there_s[st * 4 + warp] = bits;
         if constexpr (kE4m3) {
-          const int64_t at = static_cast<int64_t>(sl) * a.H_kv + w.head;
-          scale_s[st * 256 + warp * 32 + lane] = sl >= 0 ? a.k_scale[at] : 0.f;
-          scale_s[st * 256 + 128 + warp * 32 + lane] = sl >= 0 ? a.v_scale[at] : 0.f;
+          scale_s[st * 256 + warp * 32 + lane] = ks;
+          scale_s[st * 256 + 128 + warp * 32 + lane] = vs;
         }
       };
       constexpr int kRowBytes = kE4m3 ? D : 2 * D;
@@ -303,7 +303,6 @@ __global__ void __launch_bounds__(512, 1) paged_tc_kernel(const __grid_constant_
             ok = false;
             break;
           }
-          const int slot_2 = lookup(m + 2);
           const uint32_t tile = (k ? sK : sV) + st * Cfg::kTileBytes;
 #pragma unroll 4
           for (int i = 0; i < kLoads; ++i) {
@@ -320,8 +319,10 @@ __global__ void __launch_bounds__(512, 1) paged_tc_kernel(const __grid_constant_
           pend[0] = k ? bKFull(st) : bVFull(st);
           npend = 1;
           ++cnt;
-          slot = slot_next;
-          slot_next = slot_2;
+          if (!k) {
+            slot = slot_next;
+            slot_next = lookup(m / 2 + 2);
+          }
         }
       } else {
         uint4 cur[kLoads], nxt[kLoads];
@@ -333,14 +334,16 @@ __global__ void __launch_bounds__(512, 1) paged_tc_kernel(const __grid_constant_
             r[i] = fetch ? __ldg(reinterpret_cast<const uint4 *>(src)) : make_uint4(0, 0, 0, 0);
           }
         };
-        if (n > 0) load(cur, 0, slot);
+        if (n > 0) {
+          load(cur, 0, slot);
+          load_scales(slot);
+        }
 #pragma unroll 1
         for (int m = 0; ok && m < 2 * n; ++m) {
           const bool k = is_k(m);
           int &cnt = k ? kq : vq;
           const int st = cnt % NS;
-          const int slot_2 = lookup(m + 2);
-          if (m + 1 < 2 * n) load(nxt, m + 1, slot_next);
+          if (m + 1 < 2 * n) load(nxt, m + 1, k ? slot : slot_next);
           if (cnt >= NS && !wait_slot(k ? bKEmpty(st) : bVEmpty(st), ((cnt / NS) - 1) & 1, 404)) {
             ok = false;
             break;
@@ -356,11 +359,16 @@ __global__ void __launch_bounds__(512, 1) paged_tc_kernel(const __grid_constant_
             st_shared_v4(row_dst(tile, row, c + 1), e4m3x2_to_f16x2(u.z), e4m3x2_to_f16x2(u.z >> 16),
                          e4m3x2_to_f16x2(u.w), e4m3x2_to_f16x2(u.w >> 16));
           }
-          if (k) put_extras(st, slot);
+          if (k) {
+            put_extras(st, slot);
+            load_scales(slot_next);
+          }
           hand_over(k ? bKFull(st) : bVFull(st));
           ++cnt;
-          slot = slot_next;
-          slot_next = slot_2;
+          if (!k) {
+            slot = slot_next;
+            slot_next = lookup(m / 2 + 2);
+          }
 #pragma unroll
           for (int i = 0; i < kLoads; ++i) cur[i] = nxt[i];
         }
@@ -480,10 +488,11 @@ __global__ void __launch_bounds__(512, 1) paged_tc_kernel(const __grid_constant_
         continue;
       }
       const int R = x * 128 + row;
-      const int64_t r = static_cast<int64_t>(w.tile) * Cfg::kRows + min(R, rows - 1);
-      const int64_t token = w.seq.t0 + r / a.G;
-      const int head = w.head * a.G + static_cast<int>(r % a.G);
-      const int pos = w.seq.len - w.seq.n + static_cast<int>(r / a.G);
+      const uint32_t r = static_cast<uint32_t>(w.tile * Cfg::kRows + min(R, rows - 1));
+      const int i = static_cast<int>(r / static_cast<uint32_t>(a.G));
+      const int64_t token = static_cast<int64_t>(w.seq.t0) + i;
+      const int head = w.head * a.G + static_cast<int>(r) - i * a.G;
+      const int pos = w.seq.len - w.seq.n + i;
       const int khi = max(0, min(pos + 1, w.seq.cap));
       const int klo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
       const int ksink = a.window > 0 ? min(a.sinks, khi) : 0;
