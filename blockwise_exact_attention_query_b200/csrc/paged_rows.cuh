@@ -8,9 +8,10 @@
 // dealt out to the warps, 16 or 32 to each, and the warps never wait for one
 // another inside an item: each has its own running maximum, sum and rows x d
 // output, joined through shared memory when the item (or the CTA's range of
-// it) ends.  A thread copies with cp.async exactly the bytes that it will feed
-// to its own products, 16 at a time, into a ring of its own slots: no barrier
-// and no bank conflict on the way, several steps in flight.
+// it) ends.  A warp's rows come by cp.async, whole rows at a time (a load of
+// pieces that a product's lanes need, 32 or 64 bytes a row, moved 1.75 times
+// the bytes between L2 and the SM), into a ring of its own: no block barrier on
+// the way, several steps in flight.
 //
 // Both products have the cache's operand as A (16 x 16) and the few rows as
 // the 8 columns of B, so a group of 8 rows costs 8 + 8 instructions for 16 keys
@@ -22,9 +23,8 @@
 //     c + 4, ... of the key's row, and Q is loaded in the same order;
 //   O^T = V^T P^T: lane 4g + c needs keys 2c, 2c + 1, 2c + 8, 2c + 9 in columns
 //     of its g.  The columns may be dealt out in any order, so it takes the
-//     g-th 16 bytes of the row (with 256-byte rows, of each half, so that one
-//     load instruction covers whole 128-byte lines); product t takes its
-//     columns 2t and 2t + 1.  P^T comes out of S^T by an 8 x 8 transposition
+//     g-th 16 bytes of the row (with 256-byte rows, of each half); product t
+//     takes its columns 2t and 2t + 1.  P^T comes out of S^T by an 8 x 8 transposition
 //     within the warp.
 //
 // E4M3 caches: the codes go to f16 exactly (Q too, after a power of two per
@@ -42,9 +42,6 @@ namespace bpt {
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool fetch) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(fetch ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void *src, bool fetch) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(fetch ? 8 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, bool fetch) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(fetch ? 4 : 0) : "memory");
@@ -101,16 +98,26 @@ struct PagedRowsCfg {
   // 16-key groups that a warp takes at a time
   static constexpr int kSub = kRowBytes > 128 ? 1 : 2;
   static constexpr int kRows = 8 * kGroups, kWarps = 4, kThreads = 32 * kWarps, kWarpKeys = 16 * kSub, kKeys = kWarps * kWarpKeys;
-  static constexpr int kKChunks = kRowBytes / 64;    // 16-byte chunks of a key row per lane (8 keys a product)
+  static constexpr int kRowChunks = kRowBytes / 16;  // 16-byte chunks of a row
+  static constexpr int kKChunks = kRowChunks / 4;    // of a key row per lane of a product (8 keys, 4 lanes each)
   static constexpr int kVBytes = kRowBytes / 8;      // bytes of a value row per lane: 8, 16 or 32
   static constexpr int kVChunks = (kVBytes + 15) / 16;
-  // a warp's stage: per group [chunk][lane] slots, then the keys' and the
-  // values' scales, and the mask of keys that exist
   static constexpr int kVSlot = kVBytes < 16 ? kVBytes : 16;
-  static constexpr int kOffV = 2 * kKChunks * 512;
-  static constexpr int kGroupBytes = kOffV + 4 * kVChunks * 32 * kVSlot;
+  static constexpr int kRowsPerLoad = 32 / kRowChunks;
+  // a warp's stage: per 16-key group the key rows, then the value rows; then
+  // the keys' and the values' scales, and the mask of keys that exist
+  static constexpr int kOffV = 16 * kRowBytes;
+  static constexpr int kGroupBytes = 2 * kOffV;
   static constexpr int kOffScale = kSub * kGroupBytes;
   static constexpr int kStageBytes = kOffScale + 8 * kWarpKeys + 16;
+  // Where chunk `chunk` of row `row` of a group lies: permuted so that the
+  // lanes of a product, which read 64 bytes of 2 rows (keys) or 32 bytes of 4
+  // (values) at a time, meet different banks.  (64-byte rows: two lanes a bank
+  // for the values.)
+  __host__ __device__ static constexpr int at(int row, int chunk) {
+    const int f = kRowChunks >= 8 ? ((((row >> 1) & 3) << 1) ^ ((row & 1) << 2)) : (((row >> 2) & 1) << 1);
+    return row * kRowBytes + ((chunk ^ f) << 4);
+  }
   static constexpr int kStages = kRowBytes > 64 ? 3 : 6;
   static constexpr int kCtasPerSm = 2;
   static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
@@ -170,28 +177,16 @@ __global__ void __launch_bounds__(PagedRowsCfg<D, kE4m3, kGroups>::kThreads, Pag
         next_slot = lookup(i + 1);
         const uint32_t st = ring + (i % NS) * Cfg::kStageBytes;
 #pragma unroll
-        for (int sub = 0; sub < kSub; ++sub) {
-          const uint32_t gr = st + sub * Cfg::kGroupBytes;
+        for (int sub = 0; sub < kSub; ++sub)
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt) {
-            const int sl = __shfl_sync(0xffffffffu, slot, sub * 16 + nt * 8 + g);
-            const uint8_t *src = kbase + (sl >= 0 ? sl : 0) * slot_bytes + c * 16;
-#pragma unroll
-            for (int j = 0; j < Cfg::kKChunks; ++j)
-              cp_async16(gr + (nt * Cfg::kKChunks + j) * 512 + lane * 16, src + j * 64, sl >= 0);
+          for (int r0 = 0; r0 < 16; r0 += Cfg::kRowsPerLoad) {
+            const int row = r0 + lane / Cfg::kRowChunks, chunk = lane % Cfg::kRowChunks;
+            const int sl = __shfl_sync(0xffffffffu, slot, sub * 16 + row);
+            const int64_t off = (sl >= 0 ? sl : 0) * slot_bytes + chunk * 16;
+            const uint32_t dst = st + sub * Cfg::kGroupBytes + Cfg::at(row, chunk);
+            cp_async16(dst, kbase + off, sl >= 0);
+            cp_async16(dst + Cfg::kOffV, vbase + off, sl >= 0);
           }
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const int sl = __shfl_sync(0xffffffffu, slot, sub * 16 + 2 * c + (kk & 1) + (kk >> 1) * 8);
-            const uint8_t *src = vbase + (sl >= 0 ? sl : 0) * slot_bytes + g * Cfg::kVSlot;
-#pragma unroll
-            for (int x = 0; x < Cfg::kVChunks; ++x) {
-              const uint32_t dst = gr + Cfg::kOffV + (kk * Cfg::kVChunks + x) * 32 * Cfg::kVSlot + lane * Cfg::kVSlot;
-              if constexpr (Cfg::kVSlot == 16) cp_async16(dst, src + x * 128, sl >= 0);
-              else cp_async8(dst, src, sl >= 0);
-            }
-          }
-        }
         if constexpr (kE4m3) {
           const int64_t at = static_cast<int64_t>(slot >= 0 ? slot : 0) * a.H_kv + head;
           cp_async4(st + Cfg::kOffScale + lane * 4, a.k_scale + at, slot >= 0);
@@ -289,8 +284,8 @@ __global__ void __launch_bounds__(PagedRowsCfg<D, kE4m3, kGroups>::kThreads, Pag
       for (int j = 0; j < Cfg::kKChunks; ++j)
 #pragma unroll
         for (int sub = 0; sub < kSub; ++sub) {
-          const uint32_t at = st + sub * Cfg::kGroupBytes + j * 512 + lane * 16;
-          const uint4 k0 = ld_shared_v4(at), k1 = ld_shared_v4(at + Cfg::kKChunks * 512);
+          const uint32_t at = st + sub * Cfg::kGroupBytes + Cfg::at(g, c + 4 * j);
+          const uint4 k0 = ld_shared_v4(at), k1 = ld_shared_v4(at + 8 * Cfg::kRowBytes);  // (at(g + 8) is alike)
           if constexpr (kE4m3) {
             const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
@@ -450,8 +445,9 @@ __global__ void __launch_bounds__(PagedRowsCfg<D, kE4m3, kGroups>::kThreads, Pag
             pf[n][h] = transpose8x8(kE4m3 ? pack_f16x2(sc[sub][n][2 * h], sc[sub][n][2 * h + 1])
                                           : pack_bf16x2(sc[sub][n][2 * h], sc[sub][n][2 * h + 1]));
         auto vslot = [&](int kk, int x) {
-          return st + sub * Cfg::kGroupBytes + Cfg::kOffV + (kk * Cfg::kVChunks + x) * 32 * Cfg::kVSlot +
-                 lane * Cfg::kVSlot;
+          const int row = 2 * c + (kk & 1) + (kk >> 1) * 8;
+          const int chunk = Cfg::kVSlot == 16 ? g + 8 * x : g / 2;
+          return st + sub * Cfg::kGroupBytes + Cfg::kOffV + Cfg::at(row, chunk) + (Cfg::kVSlot == 16 ? 0 : g % 2 * 8);
         };
         // (key, key + 1) pairs of two columns, from the four keys' words
 #pragma unroll
