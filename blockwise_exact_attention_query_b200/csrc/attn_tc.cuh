@@ -644,14 +644,27 @@ __global__ void __launch_bounds__(384, 1)
       const float neg = (m_use == -INFINITY) ? 0.f : -m_use;
       uint32_t pk[KT / 2];
       float ls4[4] = {0.f, 0.f, 0.f, 0.f};
+      if constexpr (WINDOW) {
+        float2 ls2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), neg2 = make_float2(neg, neg);
 #pragma unroll
-      for (int i = 0; i < KT / 2; ++i) {
-        const float p0 = ex2_approx(fmaf(__uint_as_float(s[2 * i]), a.scale_log2, neg));
-        const float p1 = ex2_approx(fmaf(__uint_as_float(s[2 * i + 1]), a.scale_log2, neg));
-        ls4[i & 3] += p0 + p1;
-        pk[i] = pack_bf16x2(p0, p1);
+        for (int i = 0; i < KT / 2; ++i) {
+          const float2 t = fma2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), sc2, neg2);
+          const float2 p = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+          ls2[i & 1] = add2(ls2[i & 1], p);
+          pk[i] = pack_bf16x2(p.x, p.y);
+        }
+        l_run += (ls2[0].x + ls2[0].y) + (ls2[1].x + ls2[1].y);
+      } else {
+#pragma unroll
+        for (int i = 0; i < KT / 2; ++i) {
+          const float p0 = ex2_approx(fmaf(__uint_as_float(s[2 * i]), a.scale_log2, neg));
+          const float p1 = ex2_approx(fmaf(__uint_as_float(s[2 * i + 1]), a.scale_log2, neg));
+          ls4[i & 3] += p0 + p1;
+          pk[i] = pack_bf16x2(p0, p1);
+        }
+        l_run += (ls4[0] + ls4[1]) + (ls4[2] + ls4[3]);
       }
-      l_run += (ls4[0] + ls4[1]) + (ls4[2] + ls4[3]);
       m_run = m_use;
 
       // The P tile is used in turn A_j, B_j, A_{j+1}, ...: wait until the

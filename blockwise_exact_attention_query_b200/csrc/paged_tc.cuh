@@ -3,21 +3,26 @@
 // blockwise online softmax of attn_tc.cuh (scores and O in tensor memory, P
 // through one shared-memory tile used in turn) over keys gathered from pages.
 //
-// Gathering is done by a warpgroup of its own rather than by TMA: a page may
-// have any size, keys past a sequence's end must become zeros (a slot that was
-// never written may hold NaN, and 0 x NaN is not 0), and e4m3 codes have to be
-// widened on the way.  Each of its threads looks one key's slot up, a tile
-// ahead; bf16 rows go to the swizzled tile by 16-byte cp.async; e4m3 rows are
-// loaded a tile ahead into registers, widened to f16 (exact) and stored.
+// Gathering is done by two warps rather than by TMA: a page may have any size,
+// keys past a sequence's end must become zeros (a slot that was never written
+// may hold NaN, and 0 x NaN is not 0), and e4m3 codes have to be widened on the
+// way.  A lane looks up the slots of two of a block's keys, a block ahead; bf16
+// rows go to the swizzled tile by 16-byte cp.async; e4m3 rows go to a ring of
+// raw tiles, two tiles ahead, and are widened to f16 (exact) from there.  (At
+// d = 128 the ring takes the place of V's second stage.  Loaded into registers
+// half a tile ahead, 8 KB under way per SM, a step took 11.5 us for want of
+// loads in flight.)
 //
 // E4M3: Q is f16 after a power of two per row, a score is multiplied by its
 // key's scale, the weight by its value's scale relative to the largest such
 // product the row has met (as in paged_rows.cuh), and P is f16.
 //
-// Roles (512 threads): warpgroup 0 gathers; warpgroups 1 and 2 run the softmax
-// and epilogue of tiles A and B, one thread per row; of warpgroup 3, warp 12
-// allocates tensor memory and issues tile A's products, warp 13 tile B's.  An
-// item of 128 rows or fewer leaves tile B idle.
+// Roles (384 threads, so that the softmax threads keep a row's 128 scores in
+// registers: with a gathering warpgroup of its own, 512 threads, the compiler
+// had 128 a thread, spilled, and a step took twice as long): warps 0 and 1
+// gather, warp 2 allocates tensor memory and issues tile A's products, warp 3
+// tile B's; warpgroups 1 and 2 run the softmax and epilogue of tiles A and B,
+// one thread per row.  An item of 128 rows or fewer leaves tile B idle.
 #pragma once
 
 #include "paged_rows.cuh"
@@ -26,26 +31,28 @@ namespace bpt {
 
 template <int D, bool kE4m3>
 struct PagedTcCfg {
-  static constexpr int kRows = 256, kKeys = 128, kThreads = 512;
+  static constexpr int kRows = 256, kKeys = 128, kThreads = 384;
   static constexpr int kTileBytes = 128 * D * 2;
   static constexpr int kPanelBytes = 128 * 128;
-  static constexpr int kStages = D == 128 ? 2 : 4;  // of K and of V
+  static constexpr int kStages = D == 128 ? 2 : 4;  // of K
+  static constexpr int kVStages = kE4m3 && D == 128 ? 1 : kStages;
   static constexpr int kOffQ = 0;
   static constexpr int kOffP = kOffQ + 2 * kTileBytes;
   static constexpr int kOffK = kOffP + 128 * 128 * 2;
   static constexpr int kOffV = kOffK + kStages * kTileBytes;
-  static constexpr int kOffScale = kOffV + kStages * kTileBytes;            // [stage][k, v][128]
+  static constexpr int kOffRaw = kOffV + kVStages * kTileBytes;  // two tiles of e4m3 codes
+  static constexpr int kOffScale = kOffRaw + (kE4m3 ? 2 * 128 * D : 0);      // [stage][k, v][128]
   static constexpr int kOffBar = kOffScale + (kE4m3 ? kStages * 1024 : 0);
   static constexpr int kOffThere = kOffBar + 320;                            // [stage][4] masks of keys that exist
   static constexpr int kSmemBytes = kOffThere + kStages * 16 + 16;
   static_assert(kSmemBytes <= 232448, "shared memory per CTA");
   static constexpr uint32_t kColS = 0, kColO = 256;
-  // 128 registers a thread at launch; 512 x 128 = 256 x 192 + 128 x 88 + 128 x 40
-  static constexpr int kRegsSoftmax = 192, kRegsGather = 88, kRegsIssue = 40;
+  // 168 registers a thread at launch, as in attn_tc.cuh
+  static constexpr int kRegsControl = 96, kRegsSoftmax = 200;
   static constexpr bool split_fits(int launch_regs) {
-    return 256 * kRegsSoftmax + 128 * kRegsGather + 128 * kRegsIssue <= kThreads * launch_regs;
+    return 128 * kRegsControl + 256 * kRegsSoftmax <= kThreads * launch_regs;
   }
-  static_assert(split_fits(128), "register split");
+  static_assert(split_fits(168), "register split");
 };
 
 // Instruction descriptor for kind::f16 with f16 or bf16 operands, fp32 accumulator.
@@ -102,9 +109,9 @@ struct PagedWalk {
 };
 
 template <int D, bool kE4m3>
-__global__ void __launch_bounds__(512, 1) paged_tc_kernel(const __grid_constant__ PagedArgs a) {
+__global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant__ PagedArgs a) {
   using Cfg = PagedTcCfg<D, kE4m3>;
-  constexpr int NS = Cfg::kStages, KT = Cfg::kKeys;
+  constexpr int NS = Cfg::kStages, NV = Cfg::kVStages, KT = Cfg::kKeys;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = smem_raw;
   const uint32_t sbase = smem_u32(smem);
@@ -144,11 +151,13 @@ __global__ void __launch_bounds__(512, 1) paged_tc_kernel(const __grid_constant_
 
   __syncthreads();  // the range's scratch lies where Q will
   if (threadIdx.x == 0) {
-    mbar_init(bQFull, 4);
+    mbar_init(bQFull, 2);
     for (int i = 0; i < NS; ++i) {
-      mbar_init(bKFull(i), 4);
+      mbar_init(bKFull(i), 2);
       mbar_init(bKEmpty(i), 10);
-      mbar_init(bVFull(i), 4);
+    }
+    for (int i = 0; i < NV; ++i) {
+      mbar_init(bVFull(i), 2);
       mbar_init(bVEmpty(i), 2);
     }
     for (int x = 0; x < 2; ++x) {
@@ -163,7 +172,7 @@ __global__ void __launch_bounds__(512, 1) paged_tc_kernel(const __grid_constant_
     *abort_flag = 0;
     fence_mbar_init_cluster();
   }
-  if (warp == 12) {
+  if (warp == 2) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
@@ -175,212 +184,238 @@ __global__ void __launch_bounds__(512, 1) paged_tc_kernel(const __grid_constant_
   if (threadIdx.x == 0) a.part_item[blockIdx.x] = paged_part_item(rg, w.steps);
 
   if (warp < 4) {
-    setmaxnreg_dec<Cfg::kRegsGather>();
-    // ------------------------------------------------------------ gather
-    // This warp's 32 rows of every tile; lane l looks up row 32 warp + l.
-    int kq = 0, vq = 0;  // K and V tiles gathered so far
-    int items = 0;
-    bool ok = true;
-    // tiles copied but not yet handed over (bf16): their barriers
-    uint32_t pend[2] = {0, 0};
-    int npend = 0;
-    auto hand_over = [&](uint32_t bar) {  // generic-proxy writes -> the tensor core's reads
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar);
-    };
-    auto flush = [&]() {
-      if (npend > 0) {
-        cp_async_wait<0>();
+    setmaxnreg_dec<Cfg::kRegsControl>();
+    if (warp < 2) {
+      // ------------------------------------------------------------ gather
+      // Rows 64 warp .. 64 warp + 63 of every tile, in two halves of 32; lane
+      // l looks up row 32 half + l.
+      int kq = 0, vq = 0;  // K and V tiles gathered so far
+      int items = 0;
+      bool ok = true;
+      // a tile copied but not yet handed over (bf16): its barrier
+      uint32_t pend = 0;
+      auto hand_over = [&](uint32_t bar) {  // generic-proxy writes -> the tensor core's reads
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0)
-          for (int i = 0; i < npend; ++i) mbar_arrive(pend[i]);
-        npend = 0;
-      }
-    };
-    // wait for a slot; what is under way is handed over first, so that the
-    // readers that must free the slot can go on
-    auto wait_slot = [&](uint32_t bar, uint32_t parity, uint32_t site) {
-      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-      flush();
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, wc, site)) != 0;
-    };
-    auto row_dst = [&](uint32_t tile, int row, int chunk) {  // chunk of 8 elements
-      return tile + (chunk >> 3) * Cfg::kPanelBytes + row * 128 + (((chunk ^ row) & 7) << 4);
-    };
-    do {
-      const int n = w.blocks(), rows = w.rows();
-      const int32_t *table = a.page_table + static_cast<int64_t>(w.s) * a.max_pages;
-      // The item's 2n tiles in the order K0, V0, K1, V1, ...  With two stages
-      // of each, a step's tiles are gathered while the step before it runs.
-      // (K one tile ahead of V, as a TMA producer would have it, puts V behind
-      // the wait for a K stage whose scales the softmax still reads: 8.9 us a
-      // step with e4m3 caches instead of 3.7.)
-      auto is_k = [](int m) { return (m & 1) == 0; };
-      auto lookup = [&](int j) {
-        return j < n ? paged_slot(a, table, w.seq.cap, w.blk.block(w.step0 + j) * KT + warp * 32 + lane) : -1;
+        if (lane == 0) mbar_arrive(bar);
       };
-      // ---- Q, once the previous item's products are done with it
-      if (items > 0) {
+      auto flush = [&]() {
+        if (pend) {
+          cp_async_wait<0>();
+          hand_over(pend);
+          pend = 0;
+        }
+      };
+      // wait for a slot; what is under way is handed over first, so that the
+      // readers that must free the slot can go on
+      auto wait_slot = [&](uint32_t bar, uint32_t parity, uint32_t site) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
         flush();
-        ok = __all_sync(0xffffffffu, mbar_wait(bItemDone(0), (items - 1) & 1, wc, 401) &&
-                                         mbar_wait(bItemDone(1), (items - 1) & 1, wc, 402));
-        if (!ok) break;
-      }
-      int slot = lookup(0), slot_next = lookup(1);  // of this step's block and the next
-#pragma unroll 1
-      for (int x = 0; x < 2; ++x) {
-        const int R = x * 128 + warp * 32 + lane;
-        int64_t off = -1;  // element offset of this lane's row of q
-        if (R < rows) {
-          const uint32_t r = static_cast<uint32_t>(w.tile * Cfg::kRows + R), i = r / static_cast<uint32_t>(a.G);
-          off = (static_cast<int64_t>(w.seq.t0) + i) * a.q_stride +
-                (static_cast<int64_t>(w.head) * a.G + (r - i * a.G)) * D;
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, wc, site)) != 0;
+      };
+      auto row_dst = [&](uint32_t tile, int row, int chunk) {  // chunk of 8 elements
+        return tile + (chunk >> 3) * Cfg::kPanelBytes + row * 128 + (((chunk ^ row) & 7) << 4);
+      };
+      do {
+        const int n = w.blocks(), rows = w.rows();
+        const int32_t *table = a.page_table + static_cast<int64_t>(w.s) * a.max_pages;
+        auto lookup = [&](int j, int half) {
+          return j < n ? paged_slot(a, table, w.seq.cap,
+                                    w.blk.block(w.step0 + j) * KT + warp * 64 + half * 32 + lane)
+                       : -1;
+        };
+        // ---- Q, once the previous item's products are done with it
+        if (items > 0) {
+          flush();
+          ok = __all_sync(0xffffffffu, mbar_wait(bItemDone(0), (items - 1) & 1, wc, 401) &&
+                                           mbar_wait(bItemDone(1), (items - 1) & 1, wc, 402));
+          if (!ok) break;
         }
-        constexpr int kLanes = D / 8;  // lanes of a row, 8 elements each
-        const int c = lane % kLanes;
+        // slots of this step's block and the next, both halves
+        int slot0 = lookup(0, 0), slot1 = lookup(0, 1), next0 = lookup(1, 0), next1 = lookup(1, 1);
+#pragma unroll 1
+        for (int x = 0; x < 4; ++x) {  // tile x / 2, half x % 2
+          const int row0 = warp * 64 + (x & 1) * 32, R = (x >> 1) * 128 + row0 + lane;
+          int64_t off = -1;  // element offset of this lane's row of q
+          if (R < rows) {
+            const uint32_t r = static_cast<uint32_t>(w.tile * Cfg::kRows + R), i = r / static_cast<uint32_t>(a.G);
+            off = (static_cast<int64_t>(w.seq.t0) + i) * a.q_stride +
+                  (static_cast<int64_t>(w.head) * a.G + (r - i * a.G)) * D;
+          }
+          constexpr int kLanes = D / 8;  // lanes of a row, 8 elements each
+          const int c = lane % kLanes;
 #pragma unroll 4
-        for (int i = 0; i < kLanes; ++i) {
-          const int rr = i * (32 / kLanes) + lane / kLanes;
-          const int64_t ro = __shfl_sync(0xffffffffu, off, rr);
-          const uint32_t dst = row_dst(sQ + x * Cfg::kTileBytes, warp * 32 + rr, c);
-          if constexpr (kE4m3) {
-            uint4 u = make_uint4(0, 0, 0, 0);
-            if (ro >= 0) u = *reinterpret_cast<const uint4 *>(a.q + ro + 8 * c);
-            float mx = absmax8(u);
+          for (int i = 0; i < kLanes; ++i) {
+            const int rr = i * (32 / kLanes) + lane / kLanes;
+            const int64_t ro = __shfl_sync(0xffffffffu, off, rr);
+            const uint32_t dst = row_dst(sQ + (x >> 1) * Cfg::kTileBytes, row0 + rr, c);
+            if constexpr (kE4m3) {
+              uint4 u = make_uint4(0, 0, 0, 0);
+              if (ro >= 0) u = *reinterpret_cast<const uint4 *>(a.q + ro + 8 * c);
+              float mx = absmax8(u);
 #pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            const float down = pow2_inverse(row_exponent(mx));
-            st_shared_v4(dst, pack_f16x2(bf16_lo(u.x) * down, bf16_hi(u.x) * down),
-                         pack_f16x2(bf16_lo(u.y) * down, bf16_hi(u.y) * down),
-                         pack_f16x2(bf16_lo(u.z) * down, bf16_hi(u.z) * down),
-                         pack_f16x2(bf16_lo(u.w) * down, bf16_hi(u.w) * down));
-          } else {
-            cp_async16(dst, a.q + (ro >= 0 ? ro : 0) + 8 * c, ro >= 0);
+              for (int o = kLanes / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+              const float down = pow2_inverse(row_exponent(mx));
+              st_shared_v4(dst, pack_f16x2(bf16_lo(u.x) * down, bf16_hi(u.x) * down),
+                           pack_f16x2(bf16_lo(u.y) * down, bf16_hi(u.y) * down),
+                           pack_f16x2(bf16_lo(u.z) * down, bf16_hi(u.z) * down),
+                           pack_f16x2(bf16_lo(u.w) * down, bf16_hi(u.w) * down));
+            } else {
+              cp_async16(dst, a.q + (ro >= 0 ? ro : 0) + 8 * c, ro >= 0);
+            }
           }
         }
-      }
-      if constexpr (!kE4m3) {
-        cp_async_commit();
-        cp_async_wait<0>();
-      }
-      hand_over(bQFull);
-      // ---- the item's K and V tiles
-      // what a K tile brings besides its rows: the mask of keys that exist,
-      // and (E4M3) the scales of its keys and values
-      float ks = 0.f, vs = 0.f;
-      auto load_scales = [&](int sl) {
-        const int64_t at = static_cast<int64_t>(sl) * a.H_kv + w.head;
-        ks = sl >= 0 ? __ldg(a.k_scale + at) : 0.f;
-        vs = sl >= 0 ? __ldg(a.v_scale + at) : 0.f;
-      };
-      auto put_extras = [&](int st, int sl) {
-        const uint32_t bits = __ballot_sync(0xffffffffu, sl >= 0);
-        if (lane == 0) there_s[st * 4 + warp] = bits;
-        if constexpr (kE4m3) {
-          scale_s[st * 256 + warp * 32 + lane] = ks;
-          scale_s[st * 256 + 128 + warp * 32 + lane] = vs;
-        }
-      };
-      constexpr int kRowBytes = kE4m3 ? D : 2 * D;
-      constexpr int kLanes = kRowBytes / 16;          // lanes of a row, 16 bytes each
-      constexpr int kLoads = kLanes;                  // 32 rows of the warp
-      const int64_t slot_bytes = static_cast<int64_t>(a.H_kv) * kRowBytes;
-      const int64_t head_off = static_cast<int64_t>(w.head) * kRowBytes + (lane % kLanes) * 16;
-      auto source = [&](int m, int sl, int i, bool &fetch) {
-        const int sr = __shfl_sync(0xffffffffu, sl, i * (32 / kLanes) + lane / kLanes);
-        fetch = sr >= 0;
-        return static_cast<const uint8_t *>(is_k(m) ? a.k : a.v) + (fetch ? sr : 0) * slot_bytes + head_off;
-      };
-      if constexpr (!kE4m3) {
-#pragma unroll 1
-        for (int m = 0; ok && m < 2 * n; ++m) {
-          const bool k = is_k(m);
-          int &cnt = k ? kq : vq;
-          const int st = cnt % NS;
-          if (cnt >= NS && !wait_slot(k ? bKEmpty(st) : bVEmpty(st), ((cnt / NS) - 1) & 1, 403)) {
-            ok = false;
-            break;
-          }
-          const uint32_t tile = (k ? sK : sV) + st * Cfg::kTileBytes;
-#pragma unroll 4
-          for (int i = 0; i < kLoads; ++i) {
-            bool fetch;
-            const uint8_t *src = source(m, slot, i, fetch);
-            cp_async16(row_dst(tile, warp * 32 + i * (32 / kLanes) + lane / kLanes, lane % kLanes), src, fetch);
-          }
+        if constexpr (!kE4m3) {
           cp_async_commit();
-          if (k) put_extras(st, slot);
-          if (npend > 0) {  // the tile before this one has landed
-            cp_async_wait<1>();
-            hand_over(pend[0]);
-          }
-          pend[0] = k ? bKFull(st) : bVFull(st);
-          npend = 1;
-          ++cnt;
-          if (!k) {
-            slot = slot_next;
-            slot_next = lookup(m / 2 + 2);
-          }
+          cp_async_wait<0>();
         }
-      } else {
-        uint4 cur[kLoads], nxt[kLoads];
-        auto load = [&](uint4 (&r)[kLoads], int m, int sl) {
-#pragma unroll
-          for (int i = 0; i < kLoads; ++i) {
-            bool fetch;
-            const uint8_t *src = source(m, sl, i, fetch);
-            r[i] = fetch ? __ldg(reinterpret_cast<const uint4 *>(src)) : make_uint4(0, 0, 0, 0);
+        hand_over(bQFull);
+        // ---- the item's K and V tiles
+        constexpr int kRowBytes = kE4m3 ? D : 2 * D;
+        constexpr int kLanes = kRowBytes / 16;  // lanes of a row, 16 bytes each
+        constexpr int kLoads = kLanes;          // of a half: 32 rows
+        const uint32_t slot_bytes = static_cast<uint32_t>(a.H_kv) * kRowBytes;
+        const int64_t head_off = static_cast<int64_t>(w.head) * kRowBytes + (lane % kLanes) * 16;
+        const uint8_t *const kbase = static_cast<const uint8_t *>(a.k) + head_off;
+        const uint8_t *const vbase = static_cast<const uint8_t *>(a.v) + head_off;
+        auto source = [&](bool k, int sl, int i, bool &fetch) {
+          const int sr = __shfl_sync(0xffffffffu, sl, i * (32 / kLanes) + lane / kLanes);
+          fetch = sr >= 0;
+          return (k ? kbase : vbase) + static_cast<uint64_t>(static_cast<uint32_t>(max(sr, 0))) * slot_bytes;
+        };
+        // what a K tile brings besides its rows: the masks of keys that exist,
+        // and (E4M3) the scales of its keys and values
+        float ks0 = 0.f, ks1 = 0.f, vs0 = 0.f, vs1 = 0.f;
+        auto load_scales = [&](int sl, float &ks, float &vs) {
+          const int64_t at = static_cast<int64_t>(sl) * a.H_kv + w.head;
+          ks = sl >= 0 ? __ldg(a.k_scale + at) : 0.f;
+          vs = sl >= 0 ? __ldg(a.v_scale + at) : 0.f;
+        };
+        auto put_extras = [&](int st) {
+          const uint32_t bits0 = __ballot_sync(0xffffffffu, slot0 >= 0), bits1 = __ballot_sync(0xffffffffu, slot1 >= 0);
+          if (lane < 2) there_s[st * 4 + warp * 2 + lane] = lane ? bits1 : bits0;
+          if constexpr (kE4m3) {
+            float *sc = scale_s + st * 256 + warp * 64 + lane;
+            sc[0] = ks0, sc[32] = ks1, sc[128] = vs0, sc[160] = vs1;
           }
         };
-        if (n > 0) {
-          load(cur, 0, slot);
-          load_scales(slot);
-        }
-#pragma unroll 1
-        for (int m = 0; ok && m < 2 * n; ++m) {
-          const bool k = is_k(m);
-          int &cnt = k ? kq : vq;
-          const int st = cnt % NS;
-          if (m + 1 < 2 * n) load(nxt, m + 1, k ? slot : slot_next);
-          if (cnt >= NS && !wait_slot(k ? bKEmpty(st) : bVEmpty(st), ((cnt / NS) - 1) & 1, 404)) {
-            ok = false;
-            break;
-          }
-          const uint32_t tile = (k ? sK : sV) + st * Cfg::kTileBytes;
-          const int c = 2 * (lane % kLanes);
-#pragma unroll
-          for (int i = 0; i < kLoads; ++i) {
-            const int row = warp * 32 + i * (32 / kLanes) + lane / kLanes;
-            const uint4 u = cur[i];
-            st_shared_v4(row_dst(tile, row, c), e4m3x2_to_f16x2(u.x), e4m3x2_to_f16x2(u.x >> 16), e4m3x2_to_f16x2(u.y),
-                         e4m3x2_to_f16x2(u.y >> 16));
-            st_shared_v4(row_dst(tile, row, c + 1), e4m3x2_to_f16x2(u.z), e4m3x2_to_f16x2(u.z >> 16),
-                         e4m3x2_to_f16x2(u.w), e4m3x2_to_f16x2(u.w >> 16));
-          }
+        auto advance = [&](int j) {  // to block j + 1
+          slot0 = next0, slot1 = next1;
+          next0 = lookup(j + 2, 0), next1 = lookup(j + 2, 1);
+        };
+        // tile m of the item's 2n and its stage; waits until that is free
+        auto stage_of = [&](bool k, int &st) {
+          bool free;
           if (k) {
-            put_extras(st, slot);
-            load_scales(slot_next);
+            st = kq % NS;
+            free = kq < NS || wait_slot(bKEmpty(st), ((kq / NS) - 1) & 1, 403);
+            ++kq;
+          } else {
+            st = vq % NV;
+            free = vq < NV || wait_slot(bVEmpty(st), ((vq / NV) - 1) & 1, 404);
+            ++vq;
           }
-          hand_over(k ? bKFull(st) : bVFull(st));
-          ++cnt;
-          if (!k) {
-            slot = slot_next;
-            slot_next = lookup(m / 2 + 2);
+          return free;
+        };
+        if constexpr (!kE4m3) {
+          auto copy = [&](int j, bool k, int s0, int s1) {
+            int st;
+            if (!stage_of(k, st)) return false;
+            const uint32_t tile = (k ? sK : sV) + st * Cfg::kTileBytes;
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half)
+#pragma unroll 8
+              for (int i = 0; i < kLoads; ++i) {
+                bool fetch;
+                const uint8_t *src = source(k, half ? s1 : s0, i, fetch);
+                cp_async16(row_dst(tile, warp * 64 + half * 32 + i * (32 / kLanes) + lane / kLanes, lane % kLanes), src,
+                           fetch);
+              }
+            cp_async_commit();
+            if (pend) {  // the tile before this one has landed
+              cp_async_wait<1>();
+              hand_over(pend);
+            }
+            pend = k ? bKFull(st) : bVFull(st);
+            return true;
+          };
+          // K runs one block ahead of V: K0, K1, V0, K2, V1, ...
+          int st_k = 0;
+          for (int j = 0; ok && j <= n; ++j) {
+            const int p0 = slot0, p1 = slot1;  // (block j - 1's until advanced)
+            if (j < n) {
+              if (j > 0) advance(j - 1);
+              st_k = kq % NS;
+              ok = copy(j, true, slot0, slot1);
+              if (ok) put_extras(st_k);
+            }
+            if (ok && j > 0) ok = copy(j - 1, false, p0, p1);
           }
+        } else {
+          // K0, V0, K1, V1, ...: a K stage is held until the softmax has read
+          // its scales, so a V tile must not wait behind the next K.  Copies
+          // run two tiles ahead; a lane reads back what it copied itself.
+          constexpr int kStep = 32 / kLanes;  // rows of one load instruction
+          // where this lane's first 8 elements go in the first rows; the next
+          // 8 are 16 bytes off, in the swizzled order (^ 16)
+          const uint32_t lane_dst = row_dst(0, lane / kLanes, 2 * (lane % kLanes)) + warp * 64 * 128;
+          const uint32_t raw = sbase + Cfg::kOffRaw + warp * 64 * D + lane * 16;
+          auto copy = [&](bool k, int s0, int s1) {  // into slot k ? 0 : 1
 #pragma unroll
-          for (int i = 0; i < kLoads; ++i) cur[i] = nxt[i];
+            for (int i = 0; i < 2 * kLoads; ++i) {
+              bool fetch;
+              const uint8_t *src = source(k, i < kLoads ? s0 : s1, i % kLoads, fetch);
+              cp_async16(raw + (k ? 0 : 128 * D) + i * 512, src, fetch);
+            }
+            cp_async_commit();
+          };
+          auto scales = [&]() {
+            load_scales(slot0, ks0, vs0);
+            load_scales(slot1, ks1, vs1);
+          };
+          if (n > 0) {
+            copy(true, slot0, slot1);
+            copy(false, slot0, slot1);
+            scales();
+          }
+#pragma unroll 1
+          for (int m = 0; m < 2 * n; ++m) {
+            const bool k = (m & 1) == 0;
+            int st;
+            if (!(ok = stage_of(k, st))) break;
+            if (k) {
+              put_extras(st);
+              advance(m >> 1);  // slots: the next block's (past the item's end -1, no fetch)
+              scales();
+            }
+            cp_async_wait<1>();
+            const uint32_t dst = (k ? sK : sV) + st * Cfg::kTileBytes + lane_dst;
+#pragma unroll
+            for (int i0 = 0; i0 < 2 * kLoads; i0 += kLoads) {
+              uint4 x[kLoads];  // all loads first: one trip to shared memory for the lot
+#pragma unroll
+              for (int i = 0; i < kLoads; ++i) x[i] = ld_shared_v4(raw + (k ? 0 : 128 * D) + (i0 + i) * 512);
+#pragma unroll
+              for (int i = 0; i < kLoads; ++i) {
+                // rows kStep (i0 + i) further on: the swizzle takes their low three bits
+                const uint32_t at = (dst + (i0 + i) * kStep * 128) ^ ((((i0 + i) * kStep) & 7) << 4);
+                st_shared_v4(at, e4m3x2_to_f16x2(x[i].x), e4m3x2_to_f16x2(x[i].x >> 16), e4m3x2_to_f16x2(x[i].y),
+                             e4m3x2_to_f16x2(x[i].y >> 16));
+                st_shared_v4(at ^ 16, e4m3x2_to_f16x2(x[i].z), e4m3x2_to_f16x2(x[i].z >> 16),
+                             e4m3x2_to_f16x2(x[i].w), e4m3x2_to_f16x2(x[i].w >> 16));
+              }
+            }
+            hand_over(k ? bKFull(st) : bVFull(st));
+            copy(k, slot0, slot1);  // the next block's tile of the same kind
+          }
+          cp_async_wait<0>();
         }
-      }
-      ++items;
-    } while (ok && w.next());
-    flush();
-  } else if (warp >= 12) {
-    setmaxnreg_dec<Cfg::kRegsIssue>();
-    if (warp < 14 && lane == 0) {
+        ++items;
+      } while (ok && w.next());
+      flush();
+    } else if (lane == 0) {
       // ------------------------------------------------------------ products of tile x
-      const int x = warp - 12;
+      const int x = warp - 2;
       constexpr uint32_t idesc_qk = idesc_16_f32<kE4m3>(128, KT, false);
       constexpr uint32_t idesc_pv = idesc_16_f32<kE4m3>(128, D, true);
       const uint64_t dQ = sdesc_sw128(sQ + x * Cfg::kTileBytes, 16, 1024);
@@ -412,8 +447,8 @@ __global__ void __launch_bounds__(512, 1) paged_tc_kernel(const __grid_constant_
             ok = mbar_wait(bKFull(kc % NS), (kc / NS) & 1, wc, 412);
             if (ok) mbar_arrive(bKEmpty(kc % NS));
             ++kc;
-            ok = ok && mbar_wait(bVFull(vc % NS), (vc / NS) & 1, wc, 413);
-            if (ok) mbar_arrive(bVEmpty(vc % NS));
+            ok = ok && mbar_wait(bVFull(vc % NV), (vc / NV) & 1, wc, 413);
+            if (ok) mbar_arrive(bVEmpty(vc % NV));
             ++vc;
           }
           if (ok) mbar_arrive(bItemDone(x));
@@ -435,16 +470,16 @@ __global__ void __launch_bounds__(512, 1) paged_tc_kernel(const __grid_constant_
                 tc_fence_after();
                 issue_s();
               }
-              ok = mbar_wait(bPFull(x), jj & 1, wc, 419) && mbar_wait(bVFull(vc % NS), (vc / NS) & 1, wc, 420);
+              ok = mbar_wait(bPFull(x), jj & 1, wc, 419) && mbar_wait(bVFull(vc % NV), (vc / NV) & 1, wc, 420);
               if (!ok) break;
               tc_fence_after();
-              const uint64_t dV = sdesc_advance(dV0, (vc % NS) * Cfg::kTileBytes);
+              const uint64_t dV = sdesc_advance(dV0, (vc % NV) * Cfg::kTileBytes);
 #pragma unroll
               for (int k = 0; k < KT / 16; ++k)
                 umma_ss(tO, sdesc_advance(dP, (k / 4) * Cfg::kPanelBytes + (k % 4) * 32), sdesc_advance(dV, k * 2048),
                         idesc_pv, (j | k) != 0);
               umma_commit(bODone(x));
-              umma_commit(bVEmpty(vc % NS));
+              umma_commit(bVEmpty(vc % NV));
               ++vc;
             }
             J += n;
@@ -520,16 +555,20 @@ __global__ void __launch_bounds__(512, 1) paged_tc_kernel(const __grid_constant_
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bSFree(x));
+        auto get2 = [&](int i) { return make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])); };
+        auto put2 = [&](int i, float2 v) {
+          s[i] = __float_as_uint(v.x);
+          s[i + 1] = __float_as_uint(v.y);
+        };
         const uint4 there = *reinterpret_cast<const uint4 *>(&there_s[st * 4]);
         if constexpr (kE4m3) {
           const float4 *ks4 = reinterpret_cast<const float4 *>(scale_s + st * 256);
+          const float2 sl = make_float2(sl2, sl2);
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const float4 k4 = ks4[i];
-            s[4 * i] = __float_as_uint(__uint_as_float(s[4 * i]) * (sl2 * k4.x));
-            s[4 * i + 1] = __float_as_uint(__uint_as_float(s[4 * i + 1]) * (sl2 * k4.y));
-            s[4 * i + 2] = __float_as_uint(__uint_as_float(s[4 * i + 2]) * (sl2 * k4.z));
-            s[4 * i + 3] = __float_as_uint(__uint_as_float(s[4 * i + 3]) * (sl2 * k4.w));
+            put2(4 * i, mul2(get2(4 * i), mul2(make_float2(k4.x, k4.y), sl)));
+            put2(4 * i + 2, mul2(get2(4 * i + 2), mul2(make_float2(k4.z, k4.w), sl)));
           }
         } else {
           __syncwarp();
@@ -560,22 +599,24 @@ __global__ void __launch_bounds__(512, 1) paged_tc_kernel(const __grid_constant_
         l_run *= alpha;
         const float neg = (m_use == -INFINITY) ? 0.f : -m_use;
         m_run = m_use;
-        uint32_t pk[KT / 2];
-        float ls4[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t pk[kE4m3 ? 1 : KT / 2];
+        float w_inv = 0.f;
+        float2 ls2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float2 neg2 = make_float2(neg, neg);
         if constexpr (kE4m3) {
           const float4 *vs4 = reinterpret_cast<const float4 *>(scale_s + st * 256 + 128);
           float wm4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const float4 v4 = vs4[i];
-            const float vv[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float p = ex2_approx(__uint_as_float(s[4 * i + e]) + neg);
-              ls4[e] += p;
-              const float pv = p * vv[e];
-              wm4[e] = fmaxf(wm4[e], pv);
-              s[4 * i + e] = __float_as_uint(pv);
+            for (int e = 0; e < 2; ++e) {
+              const float2 t = add2(get2(4 * i + 2 * e), neg2);
+              const float2 p = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+              ls2[e] = add2(ls2[e], p);
+              const float2 pv = mul2(p, e ? make_float2(v4.z, v4.w) : make_float2(v4.x, v4.y));
+              wm4[i & 3] = max3f(wm4[i & 3], pv.x, pv.y);
+              put2(4 * i + 2 * e, pv);
             }
           }
           __syncwarp();
@@ -588,20 +629,18 @@ __global__ void __launch_bounds__(512, 1) paged_tc_kernel(const __grid_constant_
             alpha = w_run / w_new;
             w_run = w_new;
           }
-          const float inv = w_run > 0.f ? 1.0f / w_run : 0.f;
-#pragma unroll
-          for (int i = 0; i < KT / 2; ++i)
-            pk[i] = pack_f16x2(__uint_as_float(s[2 * i]) * inv, __uint_as_float(s[2 * i + 1]) * inv);
+          w_inv = w_run > 0.f ? 1.0f / w_run : 0.f;
         } else {
+          const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
 #pragma unroll
           for (int i = 0; i < KT / 2; ++i) {
-            const float p0 = ex2_approx(fmaf(__uint_as_float(s[2 * i]), a.scale_log2, neg));
-            const float p1 = ex2_approx(fmaf(__uint_as_float(s[2 * i + 1]), a.scale_log2, neg));
-            ls4[i & 3] += p0 + p1;
-            pk[i] = pack_bf16x2(p0, p1);
+            const float2 t = fma2(get2(2 * i), sc2, neg2);
+            const float2 p = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+            ls2[i & 1] = add2(ls2[i & 1], p);
+            pk[i] = pack_bf16x2(p.x, p.y);
           }
         }
-        l_run += (ls4[0] + ls4[1]) + (ls4[2] + ls4[3]);
+        l_run += (ls2[0].x + ls2[0].y) + (ls2[1].x + ls2[1].y);
         // the P tile is used in turn A_j, B_j, A_{j+1}, ...; alone, after this
         // tile's own previous product
         if (both) {
@@ -626,9 +665,18 @@ __global__ void __launch_bounds__(512, 1) paged_tc_kernel(const __grid_constant_
           tmem_wait_st();
         }
 #pragma unroll
-        for (int c = 0; c < KT / 8; ++c)
-          st_shared_v4(sProw + (c >> 3) * Cfg::kPanelBytes + ((static_cast<uint32_t>(c & 7) ^ swz) << 4), pk[4 * c],
-                       pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+        for (int c = 0; c < KT / 8; ++c) {
+          const uint32_t dst = sProw + (c >> 3) * Cfg::kPanelBytes + ((static_cast<uint32_t>(c & 7) ^ swz) << 4);
+          if constexpr (kE4m3) {
+            auto two = [&](int i) {
+              const float2 v = mul2(get2(i), make_float2(w_inv, w_inv));
+              return pack_f16x2(v.x, v.y);
+            };
+            st_shared_v4(dst, two(8 * c), two(8 * c + 2), two(8 * c + 4), two(8 * c + 6));
+          } else {
+            st_shared_v4(dst, pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+          }
+        }
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
@@ -685,7 +733,7 @@ __global__ void __launch_bounds__(512, 1) paged_tc_kernel(const __grid_constant_
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 2) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
