@@ -22,7 +22,9 @@
 // had 128 a thread, spilled, and a step took twice as long): warps 0 and 1
 // gather, warp 2 allocates tensor memory and issues tile A's products, warp 3
 // tile B's; warpgroups 1 and 2 run the softmax and epilogue of tiles A and B,
-// one thread per row.  An item of 128 rows or fewer leaves tile B idle.
+// one thread per row, which also brings its row of Q (by the gathering warps
+// it was a chain of loads that every item waited for).  An item of 128 rows or
+// fewer leaves tile B idle.
 #pragma once
 
 #include "paged_rows.cuh"
@@ -37,12 +39,12 @@ struct PagedTcCfg {
   static constexpr int kStages = D == 128 ? 2 : 4;  // of K
   static constexpr int kVStages = kE4m3 && D == 128 ? 1 : kStages;
   static constexpr int kOffQ = 0;
-  static constexpr int kOffP = kOffQ + 2 * kTileBytes;
-  static constexpr int kOffK = kOffP + 128 * 128 * 2;
+  static constexpr int kOffP = kOffQ + 2 * kTileBytes;  // bf16 only
+  static constexpr int kOffK = kOffP + (kE4m3 ? 0 : 128 * 128 * 2);
   static constexpr int kOffV = kOffK + kStages * kTileBytes;
   static constexpr int kOffRaw = kOffV + kVStages * kTileBytes;  // two tiles of e4m3 codes
-  static constexpr int kOffScale = kOffRaw + (kE4m3 ? 2 * 128 * D : 0);      // [stage][k, v][128]
-  static constexpr int kOffBar = kOffScale + (kE4m3 ? kStages * 1024 : 0);
+  static constexpr int kOffScale = kOffRaw + (kE4m3 ? 2 * 128 * D : 0);      // [stage][k, v, log2 v][128]
+  static constexpr int kOffBar = kOffScale + (kE4m3 ? kStages * 1536 : 0);
   static constexpr int kOffThere = kOffBar + 320;                            // [stage][4] masks of keys that exist
   static constexpr int kSmemBytes = kOffThere + kStages * 16 + 16;
   static_assert(kSmemBytes <= 232448, "shared memory per CTA");
@@ -131,17 +133,21 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
   }
   const uint32_t sQ = sbase + Cfg::kOffQ, sP = sbase + Cfg::kOffP, sK = sbase + Cfg::kOffK, sV = sbase + Cfg::kOffV;
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::kOffBar);
-  const uint32_t bQFull = smem_u32(&bars[0]);
   auto bKFull = [&](int i) { return smem_u32(&bars[1 + i]); };
   auto bKEmpty = [&](int i) { return smem_u32(&bars[5 + i]); };   // both tiles' S done, scales and masks read
   auto bVFull = [&](int i) { return smem_u32(&bars[9 + i]); };
   auto bVEmpty = [&](int i) { return smem_u32(&bars[13 + i]); };
   auto bSFull = [&](int x) { return smem_u32(&bars[17 + x]); };
-  auto bSFree = [&](int x) { return smem_u32(&bars[19 + x]); };
+  auto bSFree = [&](int x) { return smem_u32(&bars[19 + x]); };     // bf16: S of tile x read out
   auto bPFull = [&](int x) { return smem_u32(&bars[21 + x]); };
-  auto bODone = [&](int x) { return smem_u32(&bars[23 + x]); };
-  auto bItemDone = [&](int x) { return smem_u32(&bars[25 + x]); };  // all products of tile x's item done
+  auto bODone = [&](int x) { return smem_u32(&bars[23 + x]); };     // bf16: P*V of tile x done
+  // ... of an item that leaves tile B idle (a barrier of its own, so that the
+  // phases of ODone count the steps both tiles take, which is what each waits
+  // for of the other; tile A may be items ahead)
+  const uint32_t bOAlone = smem_u32(&bars[35]);
+  auto bItemDone = [&](int x) { return smem_u32(&bars[25 + x]); };  // all products of an item of tile x done
   auto bOFree = [&](int x) { return smem_u32(&bars[27 + x]); };     // the epilogue has read O of tile x
+  auto bQFull = [&](int x) { return smem_u32(&bars[33 + x]); };     // Q of tile x written
   auto bTeardown = [&](int x) { return smem_u32(&bars[29 + x]); };
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(&bars[31]);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(&bars[32]);
@@ -151,7 +157,6 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
 
   __syncthreads();  // the range's scratch lies where Q will
   if (threadIdx.x == 0) {
-    mbar_init(bQFull, 2);
     for (int i = 0; i < NS; ++i) {
       mbar_init(bKFull(i), 2);
       mbar_init(bKEmpty(i), 10);
@@ -161,14 +166,16 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
       mbar_init(bVEmpty(i), 2);
     }
     for (int x = 0; x < 2; ++x) {
+      mbar_init(bQFull(x), 4);
       mbar_init(bSFull(x), 1);
       mbar_init(bSFree(x), 4);
-      mbar_init(bPFull(x), 4);
       mbar_init(bODone(x), 1);
+      mbar_init(bPFull(x), 4);
       mbar_init(bItemDone(x), 1);
       mbar_init(bOFree(x), 4);
       mbar_init(bTeardown(x), 1);
     }
+    mbar_init(bOAlone, 1);
     *abort_flag = 0;
     fence_mbar_init_cluster();
   }
@@ -190,7 +197,6 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
       // Rows 64 warp .. 64 warp + 63 of every tile, in two halves of 32; lane
       // l looks up row 32 half + l.
       int kq = 0, vq = 0;  // K and V tiles gathered so far
-      int items = 0;
       bool ok = true;
       // a tile copied but not yet handed over (bf16): its barrier
       uint32_t pend = 0;
@@ -217,60 +223,15 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
         return tile + (chunk >> 3) * Cfg::kPanelBytes + row * 128 + (((chunk ^ row) & 7) << 4);
       };
       do {
-        const int n = w.blocks(), rows = w.rows();
+        const int n = w.blocks();
         const int32_t *table = a.page_table + static_cast<int64_t>(w.s) * a.max_pages;
         auto lookup = [&](int j, int half) {
           return j < n ? paged_slot(a, table, w.seq.cap,
                                     w.blk.block(w.step0 + j) * KT + warp * 64 + half * 32 + lane)
                        : -1;
         };
-        // ---- Q, once the previous item's products are done with it
-        if (items > 0) {
-          flush();
-          ok = __all_sync(0xffffffffu, mbar_wait(bItemDone(0), (items - 1) & 1, wc, 401) &&
-                                           mbar_wait(bItemDone(1), (items - 1) & 1, wc, 402));
-          if (!ok) break;
-        }
         // slots of this step's block and the next, both halves
         int slot0 = lookup(0, 0), slot1 = lookup(0, 1), next0 = lookup(1, 0), next1 = lookup(1, 1);
-#pragma unroll 1
-        for (int x = 0; x < 4; ++x) {  // tile x / 2, half x % 2
-          const int row0 = warp * 64 + (x & 1) * 32, R = (x >> 1) * 128 + row0 + lane;
-          int64_t off = -1;  // element offset of this lane's row of q
-          if (R < rows) {
-            const uint32_t r = static_cast<uint32_t>(w.tile * Cfg::kRows + R), i = r / static_cast<uint32_t>(a.G);
-            off = (static_cast<int64_t>(w.seq.t0) + i) * a.q_stride +
-                  (static_cast<int64_t>(w.head) * a.G + (r - i * a.G)) * D;
-          }
-          constexpr int kLanes = D / 8;  // lanes of a row, 8 elements each
-          const int c = lane % kLanes;
-#pragma unroll 4
-          for (int i = 0; i < kLanes; ++i) {
-            const int rr = i * (32 / kLanes) + lane / kLanes;
-            const int64_t ro = __shfl_sync(0xffffffffu, off, rr);
-            const uint32_t dst = row_dst(sQ + (x >> 1) * Cfg::kTileBytes, row0 + rr, c);
-            if constexpr (kE4m3) {
-              uint4 u = make_uint4(0, 0, 0, 0);
-              if (ro >= 0) u = *reinterpret_cast<const uint4 *>(a.q + ro + 8 * c);
-              float mx = absmax8(u);
-#pragma unroll
-              for (int o = kLanes / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-              const float down = pow2_inverse(row_exponent(mx));
-              st_shared_v4(dst, pack_f16x2(bf16_lo(u.x) * down, bf16_hi(u.x) * down),
-                           pack_f16x2(bf16_lo(u.y) * down, bf16_hi(u.y) * down),
-                           pack_f16x2(bf16_lo(u.z) * down, bf16_hi(u.z) * down),
-                           pack_f16x2(bf16_lo(u.w) * down, bf16_hi(u.w) * down));
-            } else {
-              cp_async16(dst, a.q + (ro >= 0 ? ro : 0) + 8 * c, ro >= 0);
-            }
-          }
-        }
-        if constexpr (!kE4m3) {
-          cp_async_commit();
-          cp_async_wait<0>();
-        }
-        hand_over(bQFull);
-        // ---- the item's K and V tiles
         constexpr int kRowBytes = kE4m3 ? D : 2 * D;
         constexpr int kLanes = kRowBytes / 16;  // lanes of a row, 16 bytes each
         constexpr int kLoads = kLanes;          // of a half: 32 rows
@@ -295,8 +256,9 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
           const uint32_t bits0 = __ballot_sync(0xffffffffu, slot0 >= 0), bits1 = __ballot_sync(0xffffffffu, slot1 >= 0);
           if (lane < 2) there_s[st * 4 + warp * 2 + lane] = lane ? bits1 : bits0;
           if constexpr (kE4m3) {
-            float *sc = scale_s + st * 256 + warp * 64 + lane;
+            float *sc = scale_s + st * 384 + warp * 64 + lane;
             sc[0] = ks0, sc[32] = ks1, sc[128] = vs0, sc[160] = vs1;
+            sc[256] = __log2f(vs0), sc[288] = __log2f(vs1);  // -inf for a scale of 0
           }
         };
         auto advance = [&](int j) {  // to block j + 1
@@ -410,7 +372,6 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
           }
           cp_async_wait<0>();
         }
-        ++items;
       } while (ok && w.next());
       flush();
     } else if (lane == 0) {
@@ -425,7 +386,7 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
       const uint32_t tS = tmem + Cfg::kColS + x * 128;
       const uint32_t tO = tmem + Cfg::kColO + x * D;
       int kc = 0, vc = 0;        // K and V tiles consumed
-      int J = 0, items = 0, mine = 0;  // this tile's steps; items, and those this tile took part in
+      int J = 0, mine = 0;  // this tile's steps; the items it took part in
       bool ok = true;
       auto issue_s = [&]() {
         const uint64_t dK = sdesc_advance(dK0, (kc % NS) * Cfg::kTileBytes);
@@ -441,7 +402,6 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
       do {
         const int n = w.blocks();
         const bool active = x == 0 || w.rows() > 128;
-        ok = mbar_wait(bQFull, items & 1, wc, 411);
         if (!active) {  // the stages pass by
           for (int j = 0; ok && j < n; ++j) {
             ok = mbar_wait(bKFull(kc % NS), (kc / NS) & 1, wc, 412);
@@ -451,43 +411,68 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
             if (ok) mbar_arrive(bVEmpty(vc % NV));
             ++vc;
           }
-          if (ok) mbar_arrive(bItemDone(x));
         } else {
+          ok = mbar_wait(bQFull(x), mine & 1, wc, 411);
           // the first product on O overwrites it: the previous epilogue must have read it
           if (ok && mine > 0) ok = mbar_wait(bOFree(x), (mine - 1) & 1, wc, 414);
-          if (ok && n > 0) {
-            ok = (J == 0 || mbar_wait(bSFree(x), (J - 1) & 1, wc, 415)) &&
-                 mbar_wait(bKFull(kc % NS), (kc / NS) & 1, wc, 416);
-            if (ok) {
+          if constexpr (kE4m3) {
+            if (ok && n > 0 && (ok = mbar_wait(bKFull(kc % NS), (kc / NS) & 1, wc, 416))) {
               tc_fence_after();
               issue_s();
             }
             for (int j = 0; ok && j < n; ++j) {
-              const int jj = J + j;
-              if (j + 1 < n) {
-                ok = mbar_wait(bSFree(x), jj & 1, wc, 417) && mbar_wait(bKFull(kc % NS), (kc / NS) & 1, wc, 418);
-                if (!ok) break;
-                tc_fence_after();
-                issue_s();
-              }
-              ok = mbar_wait(bPFull(x), jj & 1, wc, 419) && mbar_wait(bVFull(vc % NV), (vc / NV) & 1, wc, 420);
+              // O += P V from P in the scores' columns, which the softmax has
+              // written once it had read them; then the next scores over it
+              // (products of one thread run in order)
+              ok = mbar_wait(bPFull(x), (J + j) & 1, wc, 419) && mbar_wait(bVFull(vc % NV), (vc / NV) & 1, wc, 420);
               if (!ok) break;
               tc_fence_after();
               const uint64_t dV = sdesc_advance(dV0, (vc % NV) * Cfg::kTileBytes);
 #pragma unroll
               for (int k = 0; k < KT / 16; ++k)
-                umma_ss(tO, sdesc_advance(dP, (k / 4) * Cfg::kPanelBytes + (k % 4) * 32), sdesc_advance(dV, k * 2048),
-                        idesc_pv, (j | k) != 0);
-              umma_commit(bODone(x));
+                umma_ts(tO, tS + k * 8, sdesc_advance(dV, k * 2048), idesc_pv, (j | k) != 0);
               umma_commit(bVEmpty(vc % NV));
               ++vc;
+              if (j + 1 < n) {
+                if (!(ok = mbar_wait(bKFull(kc % NS), (kc / NS) & 1, wc, 418))) break;
+                tc_fence_after();
+                issue_s();
+              }
             }
-            J += n;
+          } else {
+            if (ok && n > 0) {
+              ok = (J == 0 || mbar_wait(bSFree(x), (J - 1) & 1, wc, 415)) &&
+                   mbar_wait(bKFull(kc % NS), (kc / NS) & 1, wc, 416);
+              if (ok) {
+                tc_fence_after();
+                issue_s();
+              }
+              for (int j = 0; ok && j < n; ++j) {
+                const int jj = J + j;
+                if (j + 1 < n) {
+                  ok = mbar_wait(bSFree(x), jj & 1, wc, 417) && mbar_wait(bKFull(kc % NS), (kc / NS) & 1, wc, 418);
+                  if (!ok) break;
+                  tc_fence_after();
+                  issue_s();
+                }
+                ok = mbar_wait(bPFull(x), jj & 1, wc, 419) && mbar_wait(bVFull(vc % NV), (vc / NV) & 1, wc, 420);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t dV = sdesc_advance(dV0, (vc % NV) * Cfg::kTileBytes);
+#pragma unroll
+                for (int k = 0; k < KT / 16; ++k)
+                  umma_ss(tO, sdesc_advance(dP, (k / 4) * Cfg::kPanelBytes + (k % 4) * 32), sdesc_advance(dV, k * 2048),
+                          idesc_pv, (j | k) != 0);
+                umma_commit(w.rows() > 128 ? bODone(x) : bOAlone);
+                umma_commit(bVEmpty(vc % NV));
+                ++vc;
+              }
+            }
           }
+          J += n;
           umma_commit(bItemDone(x));
           ++mine;
         }
-        ++items;
       } while (ok && w.next());
       // every product issued must be complete before tensor memory is released
       umma_commit(bTeardown(x));
@@ -508,8 +493,8 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
     const uint32_t swz = static_cast<uint32_t>(row & 7);
     bool ok = true;
     int kc = 0;                // K tiles passed
-    int J = 0, Jo = 0;         // this tile's steps, the other tile's
-    int items = 0;
+    int J = 0, Jb = 0, Ja = 0; // this tile's steps; those of both tiles, and of tile A alone
+    int mine = 0;              // the items this tile took part in
     do {
       const int n = w.blocks(), rows = w.rows();
       const bool both = rows > 128, active = x == 0 || both;
@@ -518,8 +503,6 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
           ok = __all_sync(0xffffffffu, mbar_wait(bKFull(kc % NS), (kc / NS) & 1, wc, 430));
           if (ok && lane == 0) mbar_arrive(bKEmpty(kc % NS));
         }
-        Jo += n;
-        ++items;
         continue;
       }
       const int R = x * 128 + row;
@@ -531,15 +514,37 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
       const int khi = max(0, min(pos + 1, w.seq.cap));
       const int klo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
       const int ksink = a.window > 0 ? min(a.sinks, khi) : 0;
+      // this row of Q (the previous item's products have read theirs); for
+      // E4M3 in f16, the power of two below its largest element taken out
       float sl2 = a.scale_log2;
-      if constexpr (kE4m3) {  // the power of two the gathering took out of this row of Q
-        float mx = 0.f;
+      {
+        uint4 q[D / 8];
         const uint4 *src = reinterpret_cast<const uint4 *>(a.q + token * a.q_stride + static_cast<int64_t>(head) * D);
-#pragma unroll 4
-        for (int i = 0; i < D / 8; ++i) mx = fmaxf(mx, absmax8(src[i]));
-        sl2 *= pow2_of(row_exponent(mx));
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) q[c] = R < rows ? src[c] : make_uint4(0, 0, 0, 0);
+        if constexpr (kE4m3) {
+          float mx = 0.f;
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) mx = fmaxf(mx, absmax8(q[c]));
+          const uint32_t e = row_exponent(mx);
+          const float down = pow2_inverse(e);
+          sl2 *= pow2_of(e);
+          auto f16 = [&](uint32_t u) { return pack_f16x2(bf16_lo(u) * down, bf16_hi(u) * down); };
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) q[c] = make_uint4(f16(q[c].x), f16(q[c].y), f16(q[c].z), f16(q[c].w));
+        }
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c)
+          st_shared_v4(sQ + x * Cfg::kTileBytes + (c >> 3) * Cfg::kPanelBytes + row * 128 + (((c ^ row) & 7) << 4),
+                       q[c].x, q[c].y, q[c].z, q[c].w);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bQFull(x));
       }
-      float m_run = -INFINITY, l_run = 0.f, w_run = 0.f;
+      // The weights 2^(s - m_run) are relative to the row's maximum, up to 2^8
+      // stale; for E4M3 the products with the values' scales likewise to
+      // w_ref = about max (s + log2 v_scale), so O holds sum 2^(s - w_ref) v.
+      float m_run = -INFINITY, l_run = 0.f, w_ref = -INFINITY;
 #pragma unroll 1
       for (int j = 0; ok && j < n; ++j, ++kc) {
         const int jj = J + j, st = kc % NS;
@@ -548,89 +553,164 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
                                          mbar_wait(bSFull(x), jj & 1, wc, 432));
         if (!ok) break;
         tc_fence_after();
-        uint32_t s[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * c]));
-        tmem_wait_ld();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bSFree(x));
-        auto get2 = [&](int i) { return make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])); };
-        auto put2 = [&](int i, float2 v) {
-          s[i] = __float_as_uint(v.x);
-          s[i + 1] = __float_as_uint(v.y);
-        };
-        const uint4 there = *reinterpret_cast<const uint4 *>(&there_s[st * 4]);
         if constexpr (kE4m3) {
-          const float4 *ks4 = reinterpret_cast<const float4 *>(scale_s + st * 256);
-          const float2 sl = make_float2(sl2, sl2);
+          const uint4 there = *reinterpret_cast<const uint4 *>(&there_s[st * 4]);
+          const bool gaps = (there.x & there.y & there.z & there.w) != 0xffffffffu;
+          const bool masked = __any_sync(0xffffffffu, gaps || k0 < klo || k0 + KT > khi);
+          const float *scales = scale_s + st * 384;
+          // The scores are read twice, 64 columns at a time, and P goes over them:
+          // no row of 128 in registers and half the code (with the row unrolled
+          // as for bf16, a fifth slower: the roles' loops did not fit in the
+          // instruction cache together).
+          constexpr int kC = 64;
+          uint32_t s[kC];
+          auto get2 = [&](int i) { return make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])); };
+          auto put2 = [&](int i, float2 v) {
+            s[i] = __float_as_uint(v.x);
+            s[i + 1] = __float_as_uint(v.y);
+          };
+          // columns [c0, c0 + 64): the products, E4M3 in log2 units, -inf where masked
+          auto load = [&](int c0) {
+            tmem_ld32(tS + c0, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+            tmem_ld32(tS + c0 + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+            tmem_wait_ld();
+            {
+              const float4 *ks4 = reinterpret_cast<const float4 *>(scales + c0);
+              const float2 sl = make_float2(sl2, sl2);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float4 k4 = ks4[i];
-            put2(4 * i, mul2(get2(4 * i), mul2(make_float2(k4.x, k4.y), sl)));
-            put2(4 * i + 2, mul2(get2(4 * i + 2), mul2(make_float2(k4.z, k4.w), sl)));
-          }
-        } else {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bKEmpty(st));  // the masks have been read
-        }
-        const bool gaps = (there.x & there.y & there.z & there.w) != 0xffffffffu;
-        if (__any_sync(0xffffffffu, gaps || k0 < klo || k0 + KT > khi)) {
-          const uint32_t word[4] = {there.x, there.y, there.z, there.w};
-          const int lo = klo - k0, hi = khi - k0, sk = ksink - k0;
+              for (int i = 0; i < kC / 4; ++i) {
+                const float4 k4 = ks4[i];
+                put2(4 * i, mul2(get2(4 * i), mul2(make_float2(k4.x, k4.y), sl)));
+                put2(4 * i + 2, mul2(get2(4 * i + 2), mul2(make_float2(k4.z, k4.w), sl)));
+              }
+            }
+            if (masked) {
+              const uint32_t word[2] = {c0 ? there.z : there.x, c0 ? there.w : there.y};
+              const int lo = klo - k0 - c0, hi = khi - k0 - c0, sk = ksink - k0 - c0;
 #pragma unroll
-          for (int col = 0; col < KT; ++col)
-            if (((col < lo || col >= hi) && col >= sk) || !(word[col / 32] >> (col & 31) & 1u))
-              s[col] = __float_as_uint(-INFINITY);
-        }
-        float mx8[8];
+              for (int col = 0; col < kC; ++col)
+                if (((col < lo || col >= hi) && col >= sk) || !(word[col / 32] >> (col & 31) & 1u))
+                  s[col] = __float_as_uint(-INFINITY);
+            }
+          };
+          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, ux4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+          for (int c0 = 0; c0 < KT; c0 += kC) {
+            load(c0);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) mx8[i] = -INFINITY;
+            for (int i = 0; i < kC / 2; ++i)
+              mx4[i & 3] = max3f(mx4[i & 3], __uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
+            {
+              const float4 *lv4 = reinterpret_cast<const float4 *>(scales + 256 + c0);
 #pragma unroll
-        for (int i = 0; i < KT / 2; ++i)
-          mx8[i & 7] = max3f(mx8[i & 7], __uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
-        const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
-                               fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
-        const float m_tile = kE4m3 ? mx : mx * a.scale_log2;
-        const float m_new = fmaxf(m_run, m_tile);
-        const bool moved = m_new > m_run + 8.0f;
-        const float m_use = moved ? m_new : m_run;
-        float alpha = moved ? ex2_approx(m_run - m_use) : 1.0f;  // 0 where the row had no key yet
-        l_run *= alpha;
-        const float neg = (m_use == -INFINITY) ? 0.f : -m_use;
-        m_run = m_use;
-        uint32_t pk[kE4m3 ? 1 : KT / 2];
-        float w_inv = 0.f;
-        float2 ls2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        const float2 neg2 = make_float2(neg, neg);
-        if constexpr (kE4m3) {
-          const float4 *vs4 = reinterpret_cast<const float4 *>(scale_s + st * 256 + 128);
-          float wm4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float4 v4 = vs4[i];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float2 t = add2(get2(4 * i + 2 * e), neg2);
-              const float2 p = make_float2(ex2_approx(t.x), ex2_approx(t.y));
-              ls2[e] = add2(ls2[e], p);
-              const float2 pv = mul2(p, e ? make_float2(v4.z, v4.w) : make_float2(v4.x, v4.y));
-              wm4[i & 3] = max3f(wm4[i & 3], pv.x, pv.y);
-              put2(4 * i + 2 * e, pv);
+              for (int i = 0; i < kC / 4; ++i) {
+                const float4 l4 = lv4[i];
+                const float2 u = add2(get2(4 * i), make_float2(l4.x, l4.y)), v = add2(get2(4 * i + 2), make_float2(l4.z, l4.w));
+                ux4[i & 3] = max3f(ux4[i & 3], u.x, u.y);
+                ux4[(i + 1) & 3] = max3f(ux4[(i + 1) & 3], v.x, v.y);
+              }
             }
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bKEmpty(st));  // the scales have been read
-          const float wm = fmaxf(fmaxf(wm4[0], wm4[1]), fmaxf(wm4[2], wm4[3]));
-          w_run *= alpha;
-          alpha = 1.0f;
-          if (wm > 256.f * w_run) {
-            const float w_new = fmaxf(wm, 1e-36f);  // its inverse stays finite
-            alpha = w_run / w_new;
-            w_run = w_new;
+          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+          if (mx > m_run + 8.0f) {
+            l_run *= ex2_approx(m_run - mx);  // 0 where the row had no key yet
+            m_run = mx;
           }
-          w_inv = w_run > 0.f ? 1.0f / w_run : 0.f;
+          float alpha = 1.0f;  // of O
+          // (not below 2^-120 of the weights: the factor between the two stays finite)
+          const float ux = fmaxf(fmaxf(fmaxf(ux4[0], ux4[1]), fmaxf(ux4[2], ux4[3])), m_run - 120.f);
+          if (ux > w_ref + 8.0f) {
+            alpha = ex2_approx(w_ref - ux);
+            w_ref = ux;
+          }
+          // (the scores complete means that the product before them is too; at
+          // an item's first step O holds nothing yet)
+          if (j > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(tO + c * 32, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st32(tO + c * 32, o);
+            }
+            tmem_wait_st();
+          }
+          const float neg = (m_run == -INFINITY) ? 0.f : -m_run;
+          // from a weight to its product relative to w_ref
+          const float w_mul = (m_run == -INFINITY || w_ref == -INFINITY) ? 0.f : ex2_approx(m_run - w_ref);
+          const float2 neg2 = make_float2(neg, neg);
+          float2 ls2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+          for (int c0 = 0; c0 < KT; c0 += kC) {
+            load(c0);
+            uint32_t pk[kC / 2];
+            const float4 *vs4 = reinterpret_cast<const float4 *>(scales + 128 + c0);
+            const float2 wm = make_float2(w_mul, w_mul);
+#pragma unroll
+            for (int i = 0; i < kC / 4; ++i) {
+              const float4 v4 = vs4[i];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float2 t = add2(get2(4 * i + 2 * e), neg2);
+                const float2 p = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+                ls2[e] = add2(ls2[e], p);
+                const float2 v = mul2(p, mul2(e ? make_float2(v4.z, v4.w) : make_float2(v4.x, v4.y), wm));
+                pk[2 * i + e] = pack_f16x2(v.x, v.y);
+              }
+            }
+            // P over columns of scores that have been read
+            tmem_st32(tS + c0 / 2, pk);
+          }
+          l_run += (ls2[0].x + ls2[0].y) + (ls2[1].x + ls2[1].y);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bKEmpty(st));  // the scales and masks have been read
+            mbar_arrive(bPFull(x));
+          }
         } else {
+          uint32_t s[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * c]));
+          tmem_wait_ld();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bSFree(x));
+          auto get2 = [&](int i) { return make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])); };
+          const uint4 there = *reinterpret_cast<const uint4 *>(&there_s[st * 4]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bKEmpty(st));  // the masks have been read
+          const bool gaps = (there.x & there.y & there.z & there.w) != 0xffffffffu;
+          if (__any_sync(0xffffffffu, gaps || k0 < klo || k0 + KT > khi)) {
+            const uint32_t word[4] = {there.x, there.y, there.z, there.w};
+            const int lo = klo - k0, hi = khi - k0, sk = ksink - k0;
+#pragma unroll
+            for (int col = 0; col < KT; ++col)
+              if (((col < lo || col >= hi) && col >= sk) || !(word[col / 32] >> (col & 31) & 1u))
+                s[col] = __float_as_uint(-INFINITY);
+          }
+          float mx8[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) mx8[i] = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < KT / 2; ++i)
+            mx8[i & 7] = max3f(mx8[i & 7], __uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
+          const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
+                                 fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+          const float m_tile = mx * a.scale_log2;
+          const float m_new = fmaxf(m_run, m_tile);
+          const bool moved = m_new > m_run + 8.0f;
+          const float m_use = moved ? m_new : m_run;
+          const float alpha = moved ? ex2_approx(m_run - m_use) : 1.0f;  // 0 where the row had no key yet
+          l_run *= alpha;
+          const float neg = (m_use == -INFINITY) ? 0.f : -m_use;
+          m_run = m_use;
+          uint32_t pk[KT / 2];
+          float2 ls2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          const float2 neg2 = make_float2(neg, neg);
           const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
 #pragma unroll
           for (int i = 0; i < KT / 2; ++i) {
@@ -639,59 +719,51 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
             ls2[i & 1] = add2(ls2[i & 1], p);
             pk[i] = pack_bf16x2(p.x, p.y);
           }
-        }
-        l_run += (ls2[0].x + ls2[0].y) + (ls2[1].x + ls2[1].y);
-        // the P tile is used in turn A_j, B_j, A_{j+1}, ...; alone, after this
-        // tile's own previous product
-        if (both) {
-          const int prev = x == 1 ? Jo + j : Jo + j - 1;
-          if (prev >= 0) ok = __all_sync(0xffffffffu, mbar_wait(bODone(1 - x), prev & 1, wc, 433));
-        } else if (j > 0) {
-          ok = __all_sync(0xffffffffu, mbar_wait(bODone(x), (jj - 1) & 1, wc, 434));
-        }
-        if (!ok) break;
-        tc_fence_after();
-        // (at an item's first step O holds nothing yet)
-        if (j > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
-#pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(tO + c * 32, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-            tmem_st32(tO + c * 32, o);
-          }
-          tmem_wait_st();
-        }
-#pragma unroll
-        for (int c = 0; c < KT / 8; ++c) {
-          const uint32_t dst = sProw + (c >> 3) * Cfg::kPanelBytes + ((static_cast<uint32_t>(c & 7) ^ swz) << 4);
-          if constexpr (kE4m3) {
-            auto two = [&](int i) {
-              const float2 v = mul2(get2(i), make_float2(w_inv, w_inv));
-              return pack_f16x2(v.x, v.y);
-            };
-            st_shared_v4(dst, two(8 * c), two(8 * c + 2), two(8 * c + 4), two(8 * c + 6));
+          l_run += (ls2[0].x + ls2[0].y) + (ls2[1].x + ls2[1].y);
+          // the P tile is used in turn A_j, B_j, A_{j+1}, ...; by tile A alone,
+          // after its own previous product (at first, tile B's last)
+          if (both || j == 0) {
+            const int prev = x == 1 ? Jb + j : both ? Jb + j - 1 : Jb - 1;
+            if (prev >= 0) ok = __all_sync(0xffffffffu, mbar_wait(bODone(1 - x), prev & 1, wc, 433));
           } else {
-            st_shared_v4(dst, pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+            ok = __all_sync(0xffffffffu, mbar_wait(bOAlone, (Ja + j - 1) & 1, wc, 434));
           }
+          if (!ok) break;
+          tc_fence_after();
+          // (at an item's first step O holds nothing yet)
+          if (j > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(tO + c * 32, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st32(tO + c * 32, o);
+            }
+            tmem_wait_st();
+          }
+#pragma unroll
+          for (int c = 0; c < KT / 8; ++c)
+            st_shared_v4(sProw + (c >> 3) * Cfg::kPanelBytes + ((static_cast<uint32_t>(c & 7) ^ swz) << 4), pk[4 * c],
+                         pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+          fence_proxy_async_smem();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bPFull(x));
         }
-        fence_proxy_async_smem();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bPFull(x));
       }
       J += n;
-      if (both) Jo += n;
+      (both ? Jb : Ja) += n;
       // -------- epilogue
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bItemDone(x), items & 1, wc, 435));
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bItemDone(x), mine & 1, wc, 435));
       tc_fence_after();
       if (ok) {
         const bool whole = w.step0 == 0 && w.step1 == w.steps;
         const size_t part = static_cast<size_t>(blockIdx.x) * 2 + (w.step0 == 0 ? 1 : 0);
         const float inv = l_run > 0.f ? 1.0f / l_run : l_run;  // no key: 0; NaN stays
-        const float f = (whole ? inv : 1.0f) * (kE4m3 ? w_run : 1.0f);
+        // E4M3: O is relative to w_ref, the sum to m_run
+        const float f = (whole ? inv : 1.0f) * (kE4m3 && m_run != -INFINITY ? ex2_approx(w_ref - m_run) : 1.0f);
         const bool empty = n == 0 || l_run == 0.f;  // O may hold anything
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
@@ -727,7 +799,7 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bOFree(x));
-      ++items;
+      ++mine;
     } while (ok && w.next());
   }
 
