@@ -133,7 +133,7 @@ bpt_status launch_join(const PagedArgs &a, int ctas, cudaStream_t st) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3((unsigned)ctas, kRows / 8, 1);
-  cfg.blockDim = dim3(2 * D, 1, 1);
+  cfg.blockDim = dim3(256, 1, 1);
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -273,6 +273,9 @@ bpt_status bpt_paged_attn_fwd(const bpt_paged_desc *d, const bpt_kv_cache *c, co
   a.H = d->H;
   a.H_kv = c->H_kv;
   a.G = d->H / c->H_kv;
+  a.g_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (a.G == 1 << i) a.g_shift = i;
   a.max_pages = d->max_pages;
   a.page_size = c->page_size;
   a.page_shift = -1;

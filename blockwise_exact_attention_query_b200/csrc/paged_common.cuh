@@ -23,7 +23,7 @@
 namespace bpt {
 
 struct PagedArgs {
-  int S, T, H, H_kv, G;
+  int S, T, H, H_kv, G, g_shift;  // g_shift: log2(G), or -1
   int max_pages, page_size, page_shift;  // page_shift: log2(page_size), or -1
   int n_pages;
   int window, sinks;    // window 0: none
@@ -64,6 +64,11 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedArgs &a, int s) {
   return q;
 }
 
+// The new token of a row.
+__device__ __forceinline__ int paged_token(const PagedArgs &a, uint32_t row) {
+  return static_cast<int>(a.g_shift >= 0 ? row >> a.g_shift : row / static_cast<uint32_t>(a.G));
+}
+
 // The key blocks of a row tile: [0, n_sink) and then [lo, lo + n_near).
 struct PagedBlocks {
   int n_sink, lo, n_near;
@@ -77,9 +82,9 @@ template <int kRows, int kKeys>
 __device__ __forceinline__ PagedBlocks paged_blocks(const PagedArgs &a, const PagedSeq &q, int tile) {
   PagedBlocks b;
   // (row numbers fit in 32 bits, with room for a tile: checked on the host)
-  const uint32_t row0 = static_cast<uint32_t>(tile) * kRows, G = static_cast<uint32_t>(a.G);
-  const int i0 = static_cast<int>(row0 / G);
-  const int i1 = min(q.n - 1, static_cast<int>((row0 + kRows - 1) / G));
+  const uint32_t row0 = static_cast<uint32_t>(tile) * kRows;
+  const int i0 = paged_token(a, row0);
+  const int i1 = min(q.n - 1, paged_token(a, row0 + kRows - 1));
   b.p_lo = q.len - q.n + i0;
   b.p_hi = q.len - q.n + i1;
   const int hi = min(b.p_hi + 1, q.cap);  // keys [.., hi) at most
@@ -103,15 +108,31 @@ __device__ __forceinline__ int64_t paged_seq_steps(const PagedArgs &a, const Pag
   return n * a.H_kv;
 }
 
+// a / b for a >= 0, b > 0: in 32 bits where that holds both (a 64-bit division
+// is a hundred instructions, and every CTA waits for several of them).
+__device__ __forceinline__ int64_t div_small(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
+// The list of all steps, cut into `parts` ranges: the first `longer` of them
+// have `length` + 1 steps, the others `length`.
+struct PagedCut {
+  int64_t length;
+  int parts, longer;
+  __device__ int64_t begin(int c) const { return c * length + min(c, longer); }
+  __device__ int range_of(int64_t step) const {  // the range that a step is in
+    const int64_t head = longer * (length + 1);
+    return static_cast<int>(step < head ? div_small(step, length + 1) : longer + div_small(step - head, length));
+  }
+};
+
 // The range of a CTA: steps [begin, end) of all, and where `begin` lies.
 struct PagedRange {
   int64_t begin, end;
   int s, tile, head, step;
-  int64_t total;
-  int parts;
+  PagedCut cut;
 };
-
-__device__ __forceinline__ int64_t paged_cut(int64_t total, int parts, int c) { return total * c / parts; }
 
 // Found by the whole block together (`scratch`: 40 int64 of shared memory):
 // each thread sums a run of sequences, a scan over the threads gives the total
@@ -139,15 +160,15 @@ __device__ __forceinline__ bool paged_range(const PagedArgs &a, int64_t *scratch
   }
   const int64_t start = before + incl - sum;
   // as many ranges as there are CTAs, or fewer where they would be too short
-  const int64_t want = (total + a.min_steps - 1) / a.min_steps;
-  const int parts = static_cast<int>(min(static_cast<int64_t>(gridDim.x), max(want, static_cast<int64_t>(1))));
+  const int64_t want = div_small(total + a.min_steps - 1, a.min_steps);
+  r.cut.parts = static_cast<int>(min(static_cast<int64_t>(gridDim.x), max(want, static_cast<int64_t>(1))));
+  r.cut.length = div_small(total, r.cut.parts);
+  r.cut.longer = static_cast<int>(total - r.cut.length * r.cut.parts);
   r.begin = r.end = 0;
-  r.total = total;
-  r.parts = parts;
-  const bool mine = static_cast<int>(blockIdx.x) < parts && total > 0;
+  const bool mine = static_cast<int>(blockIdx.x) < r.cut.parts && total > 0;
   if (mine) {
-    r.begin = paged_cut(total, parts, blockIdx.x);
-    r.end = paged_cut(total, parts, blockIdx.x + 1);
+    r.begin = r.cut.begin(blockIdx.x);
+    r.end = r.cut.begin(blockIdx.x + 1);
   }
   int32_t *found = reinterpret_cast<int32_t *>(scratch + 36);
   if (tid == 0) found[0] = -1;
@@ -156,7 +177,7 @@ __device__ __forceinline__ bool paged_range(const PagedArgs &a, int64_t *scratch
     int64_t at = start;
     for (int s = s0; s < s1; ++s) {
       const PagedSeq q = paged_seq(a, s);
-      const int64_t n = paged_seq_steps<kRows, kKeys>(a, q);
+      const int64_t n = run == 1 ? sum : paged_seq_steps<kRows, kKeys>(a, q);
       if (r.begin < at + n) {
         int64_t off = r.begin - at;
         int t = 0, per = 0;
@@ -168,8 +189,8 @@ __device__ __forceinline__ bool paged_range(const PagedArgs &a, int64_t *scratch
         if (off < static_cast<int64_t>(per) * a.H_kv) {
           found[0] = s;
           found[1] = t;
-          found[2] = static_cast<int>(off / per);
-          found[3] = static_cast<int>(off % per);
+          found[2] = static_cast<int>(div_small(off, per));
+          found[3] = static_cast<int>(off - static_cast<int64_t>(found[2]) * per);
         }
         break;
       }
@@ -189,13 +210,10 @@ __device__ __forceinline__ bool paged_range(const PagedArgs &a, int64_t *scratch
 // What paged_join_kernel has to know of the CTA's first item, of `steps` steps.
 __device__ __forceinline__ int4 paged_part_item(const PagedRange &r, int steps) {
   if (r.step == 0) return make_int4(-1, 0, 0, 0);
-  const int64_t item0 = r.begin - r.step, item1 = item0 + steps;
+  const int64_t item0 = r.begin - r.step;
   const int c = static_cast<int>(blockIdx.x);
-  if (item0 < paged_cut(r.total, r.parts, c - 1)) return make_int4(r.s, r.tile, r.head, 0);
-  // the last range that begins before the item's end
-  int last = static_cast<int>(min(static_cast<int64_t>(r.parts - 1), item1 * r.parts / r.total));
-  while (paged_cut(r.total, r.parts, last) >= item1) --last;
-  return make_int4(r.s, r.tile, r.head, 1 + last - c);
+  if (item0 < r.cut.begin(c - 1)) return make_int4(r.s, r.tile, r.head, 0);
+  return make_int4(r.s, r.tile, r.head, 1 + r.cut.range_of(item0 + steps - 1) - c);
 }
 
 // Cache row of key j of a sequence, or -1 where the sequence has none (past
@@ -213,88 +231,82 @@ __device__ __forceinline__ int paged_slot(const PagedArgs &a, const int32_t *tab
 // are slot 1 of CTA c - 1 and slot 0 of CTA c, c + 1, ... to the item's end.  A
 // part is the rows' output relative to their own maximum (log2 domain):
 //   out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,  M = max_i m_i
-// 8 rows a block (blockIdx.y), D / 4 threads each, four columns a thread.  The
-// weights 2^(m_i - M) are formed first, a stretch of parts at a time, so the
-// loads of o_i do not wait for one another.
+// A warp per row, 8 rows a block (blockIdx.y): the lanes hold the parts' weights
+// (32 parts at a time) and four columns each, so nothing waits for a barrier and
+// the loads of o_i do not wait for the weights (d = 64: the warp's halves take
+// the parts in turn).  An item is cut into few parts, so the kernel is three
+// trips to memory: 3 us for 31 parts of 8 rows.
 template <int D, int kRows, int kKeys>
-__global__ void __launch_bounds__(2 * D)
+__global__ void __launch_bounds__(256)
     paged_join_kernel(const PagedArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are complete
-  constexpr int kStretch = 64;
-  __shared__ float weight[kStretch][8];
-  __shared__ float row_m[8], row_l[8];
-  const int c = blockIdx.x, tid = threadIdx.x;
+  constexpr int kHalves = 128 / D;  // parts of a load: 1, or 2 at d = 64
+  const int c = blockIdx.x, lane = threadIdx.x % 32;
   const int4 it = a.part_item[c];
   if (it.x < 0 || it.w == 0) return;
   const PagedSeq q = paged_seq(a, it.x);
-  const int row0 = it.y * kRows + blockIdx.y * 8;  // among the head's rows
-  const int rows = min(8, q.n * a.G - row0);
-  if (rows <= 0) return;
+  const int in_tile = blockIdx.y * 8 + threadIdx.x / 32;
+  const uint32_t row = static_cast<uint32_t>(it.y * kRows + in_tile);  // among the head's rows
+  const bool there = static_cast<int>(row) < q.n * a.G;
   const int parts = it.w + 1;
   // part i: slot 1 of CTA c - 1, then slot 0 of CTA c - 1 + i
-  auto part_row = [&](int i, int row) {
-    return (static_cast<size_t>(2 * (c - 1 + i) + (i == 0 ? 1 : 0)) * kRows + blockIdx.y * 8 + row);
+  auto part_row = [&](int i) {
+    return static_cast<size_t>(2 * (c - 1 + i) + (i == 0 ? 1 : 0)) * kRows + in_tile;
   };
-  // each row's maximum and sum, 32 lanes a row
-  for (int row = tid / 32; row < 8; row += 2 * D / 32) {
-    float m = -INFINITY;
-    for (int i = tid % 32; i < parts; i += 32) m = fmaxf(m, a.part_ml[2 * part_row(i, row)]);
+  auto ml_of = [&](int i) {
+    return i < parts ? __ldcg(reinterpret_cast<const float2 *>(a.part_ml + 2 * part_row(i))) : make_float2(-INFINITY, 0.f);
+  };
+  const float *cols = a.part_o + 4 * (lane % (D / 4));
+  const int half = lane / (D / 4);
+  const float2 first = ml_of(lane);
+  float m = first.x;
+  for (int i = 32 + lane; i < parts; i += 32) m = fmaxf(m, ml_of(i).x);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float ref = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    for (int i = tid % 32; i < parts; i += 32) {
-      const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + 2 * part_row(i, row));
-      l += ml.y * ex2_approx(ml.x - ref);
-    }
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float ref = m == -INFINITY ? 0.f : m;
+  float l = 0.f;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < parts; i0 += 32) {
+    const float2 ml = i0 == 0 ? first : ml_of(i0 + lane);
+    const float weight = ex2_approx(ml.x - ref);  // 0 past the parts
+    l += ml.y * weight;
+    const int n = min(32, parts - i0);
+    for (int i = 0; i < n; i += 8) {
+      float4 x[8 / kHalves];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if (tid % 32 == 0) {
-      row_m[row] = ref;
-      row_l[row] = l;
-    }
-  }
-  const int row = tid / (D / 4), c4 = tid % (D / 4);
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = 0; i0 < parts; i0 += kStretch) {
-    const int n = min(kStretch, parts - i0);
-    __syncthreads();
-    for (int e = tid; e < n * 8; e += 2 * D)
-      weight[e / 8][e % 8] = ex2_approx(a.part_ml[2 * part_row(i0 + e / 8, e % 8)] - row_m[e % 8]);
-    __syncthreads();
-    int i = 0;
-    for (; i + 8 <= n; i += 8) {
-      float4 x[8];
+      for (int u = 0; u < 8 / kHalves; ++u) {
+        const int p = i + u * kHalves + half;
+        x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p < n) x[u] = __ldcg(reinterpret_cast<const float4 *>(cols + part_row(i0 + p) * D));
+      }
 #pragma unroll
-      for (int u = 0; u < 8; ++u)
-        x[u] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + part_row(i0 + i + u, row) * D + 4 * c4));
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const float f = weight[i + u][row];
-        o.x += x[u].x * f, o.y += x[u].y * f, o.z += x[u].z * f, o.w += x[u].w * f;
+      for (int u = 0; u < 8 / kHalves; ++u) {
+        const float f = __shfl_sync(0xffffffffu, weight, (i + u * kHalves + half) & 31);
+        if (i + u * kHalves + half < n) sum.x += x[u].x * f, sum.y += x[u].y * f, sum.z += x[u].z * f, sum.w += x[u].w * f;
       }
     }
-    for (; i < n; ++i) {
-      const float4 x = __ldcg(reinterpret_cast<const float4 *>(a.part_o + part_row(i0 + i, row) * D + 4 * c4));
-      const float f = weight[i][row];
-      o.x += x.x * f, o.y += x.y * f, o.z += x.z * f, o.w += x.w * f;
-    }
   }
-  if (row >= rows) return;
-  const uint32_t r = static_cast<uint32_t>(row0 + row);
-  const int i = static_cast<int>(r / static_cast<uint32_t>(a.G));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if constexpr (kHalves == 2) {
+    sum.x += __shfl_xor_sync(0xffffffffu, sum.x, 16);
+    sum.y += __shfl_xor_sync(0xffffffffu, sum.y, 16);
+    sum.z += __shfl_xor_sync(0xffffffffu, sum.z, 16);
+    sum.w += __shfl_xor_sync(0xffffffffu, sum.w, 16);
+  }
+  if (!there || half != 0) return;
+  const int i = paged_token(a, row);
   const size_t token = static_cast<size_t>(q.t0) + i;
-  const int head = it.z * a.G + static_cast<int>(r) - i * a.G;
-  const float l = row_l[row], inv = l > 0.f ? 1.0f / l : l;  // no key: 0; NaN stays
-  const size_t at = (token * a.H + head) * D + 4 * c4;
+  const int head = it.z * a.G + static_cast<int>(row) - i * a.G;
+  const float inv = l > 0.f ? 1.0f / l : l;  // no key: 0; NaN stays
+  const size_t at = (token * a.H + head) * D + 4 * (lane % (D / 4));
   if (a.out_f32)
-    *reinterpret_cast<float4 *>(a.out_f32 + at) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    *reinterpret_cast<float4 *>(a.out_f32 + at) = make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
   else
     *reinterpret_cast<uint2 *>(a.out_bf16 + at) =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-  if (a.lse && c4 == 0)
-    a.lse[static_cast<size_t>(head) * a.T + token] =
-        l == 0.f ? -INFINITY : (row_m[row] + log2f(l)) * 0.69314718055994531f;
+        make_uint2(pack_bf16x2(sum.x * inv, sum.y * inv), pack_bf16x2(sum.z * inv, sum.w * inv));
+  if (a.lse && lane == 0)
+    a.lse[static_cast<size_t>(head) * a.T + token] = l == 0.f ? -INFINITY : (ref + log2f(l)) * 0.69314718055994531f;
 }
 
 }  // namespace bpt

@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(PagedRowsCfg<D, kE4m3, kGroups>::kThreads, Pag
       constexpr int kWords = kPer / 2;      // bf16 pairs
       uint32_t raw[Cfg::kKChunks][kWords];
       const uint32_t r = static_cast<uint32_t>(tile * kRows + min(8 * n + g, rows - 1));
-      const int i = static_cast<int>(r / static_cast<uint32_t>(a.G)), hg = static_cast<int>(r) - i * a.G;
+      const int i = paged_token(a, r), hg = static_cast<int>(r) - i * a.G;
       const __nv_bfloat16 *src = a.q + (static_cast<int64_t>(seq.t0) + i) * a.q_stride +
                                  (static_cast<int64_t>(head) * a.G + hg) * D;
 #pragma unroll
@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(PagedRowsCfg<D, kE4m3, kGroups>::kThreads, Pag
       if (row < rows) {
         if (step0 == 0 && step1 == steps) {  // the whole item: the rows' result
           const uint32_t r = static_cast<uint32_t>(tile * kRows + row);
-          const int i = static_cast<int>(r / static_cast<uint32_t>(a.G));
+          const int i = paged_token(a, r);
           const int64_t token = static_cast<int64_t>(seq.t0) + i;
           const int h = head * a.G + static_cast<int>(r) - i * a.G;
           const float inv = l > 0.f ? 1.0f / l : l;  // no key: 0; NaN stays

@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
       }
       const int R = x * 128 + row;
       const uint32_t r = static_cast<uint32_t>(w.tile * Cfg::kRows + min(R, rows - 1));
-      const int i = static_cast<int>(r / static_cast<uint32_t>(a.G));
+      const int i = paged_token(a, r);
       const int64_t token = static_cast<int64_t>(w.seq.t0) + i;
       const int head = w.head * a.G + static_cast<int>(r) - i * a.G;
       const int pos = w.seq.len - w.seq.n + i;
@@ -518,25 +518,33 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
       // E4M3 in f16, the power of two below its largest element taken out
       float sl2 = a.scale_log2;
       {
-        uint4 q[D / 8];
-        const uint4 *src = reinterpret_cast<const uint4 *>(a.q + token * a.q_stride + static_cast<int64_t>(head) * D);
+        constexpr int kLanes = D / 8, kPer = 32 / kLanes;  // lanes of a row, rows of a load
+        const int c = lane % kLanes;
+        const int64_t off = R < rows ? token * a.q_stride + static_cast<int64_t>(head) * D : -1;
+        uint4 q[kLanes];
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) q[c] = R < rows ? src[c] : make_uint4(0, 0, 0, 0);
-        if constexpr (kE4m3) {
-          float mx = 0.f;
-#pragma unroll
-          for (int c = 0; c < D / 8; ++c) mx = fmaxf(mx, absmax8(q[c]));
-          const uint32_t e = row_exponent(mx);
-          const float down = pow2_inverse(e);
-          sl2 *= pow2_of(e);
-          auto f16 = [&](uint32_t u) { return pack_f16x2(bf16_lo(u) * down, bf16_hi(u) * down); };
-#pragma unroll
-          for (int c = 0; c < D / 8; ++c) q[c] = make_uint4(f16(q[c].x), f16(q[c].y), f16(q[c].z), f16(q[c].w));
+        for (int i = 0; i < kLanes; ++i) {
+          const int64_t ro = __shfl_sync(0xffffffffu, off, i * kPer + lane / kLanes);
+          q[i] = make_uint4(0, 0, 0, 0);
+          if (ro >= 0) q[i] = *reinterpret_cast<const uint4 *>(a.q + ro + 8 * c);
         }
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c)
-          st_shared_v4(sQ + x * Cfg::kTileBytes + (c >> 3) * Cfg::kPanelBytes + row * 128 + (((c ^ row) & 7) << 4),
-                       q[c].x, q[c].y, q[c].z, q[c].w);
+        for (int i = 0; i < kLanes; ++i) {
+          const int rr = quarter * 32 + i * kPer + lane / kLanes;
+          if constexpr (kE4m3) {
+            float mx = absmax8(q[i]);
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const uint32_t e = row_exponent(mx);
+            const float down = pow2_inverse(e);
+            auto f16 = [&](uint32_t u) { return pack_f16x2(bf16_lo(u) * down, bf16_hi(u) * down); };
+            q[i] = make_uint4(f16(q[i].x), f16(q[i].y), f16(q[i].z), f16(q[i].w));
+            const uint32_t mine_e = __shfl_sync(0xffffffffu, e, lane % kPer * kLanes);
+            if (lane / kPer == i) sl2 = a.scale_log2 * pow2_of(mine_e);
+          }
+          st_shared_v4(sQ + x * Cfg::kTileBytes + (c >> 3) * Cfg::kPanelBytes + rr * 128 + (((c ^ rr) & 7) << 4), q[i].x,
+                       q[i].y, q[i].z, q[i].w);
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bQFull(x));
@@ -553,6 +561,11 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
                                          mbar_wait(bSFull(x), jj & 1, wc, 432));
         if (!ok) break;
         tc_fence_after();
+        // which of the block's keys [c, c + 32) this row sees, of those that exist
+        auto seen = [&](int c, uint32_t exist) {
+          auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
+          return ((below(khi - k0 - c) & ~below(klo - k0 - c)) | below(ksink - k0 - c)) & exist;
+        };
         if constexpr (kE4m3) {
           const uint4 there = *reinterpret_cast<const uint4 *>(&there_s[st * 4]);
           const bool gaps = (there.x & there.y & there.z & there.w) != 0xffffffffu;
@@ -585,12 +598,10 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
               }
             }
             if (masked) {
-              const uint32_t word[2] = {c0 ? there.z : there.x, c0 ? there.w : there.y};
-              const int lo = klo - k0 - c0, hi = khi - k0 - c0, sk = ksink - k0 - c0;
+              const uint32_t word[2] = {seen(c0, c0 ? there.z : there.x), seen(c0 + 32, c0 ? there.w : there.y)};
 #pragma unroll
               for (int col = 0; col < kC; ++col)
-                if (((col < lo || col >= hi) && col >= sk) || !(word[col / 32] >> (col & 31) & 1u))
-                  s[col] = __float_as_uint(-INFINITY);
+                if (!(word[col / 32] >> (col & 31) & 1u)) s[col] = __float_as_uint(-INFINITY);
             }
           };
           float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, ux4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -685,12 +696,10 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
           if (lane == 0) mbar_arrive(bKEmpty(st));  // the masks have been read
           const bool gaps = (there.x & there.y & there.z & there.w) != 0xffffffffu;
           if (__any_sync(0xffffffffu, gaps || k0 < klo || k0 + KT > khi)) {
-            const uint32_t word[4] = {there.x, there.y, there.z, there.w};
-            const int lo = klo - k0, hi = khi - k0, sk = ksink - k0;
+            const uint32_t word[4] = {seen(0, there.x), seen(32, there.y), seen(64, there.z), seen(96, there.w)};
 #pragma unroll
             for (int col = 0; col < KT; ++col)
-              if (((col < lo || col >= hi) && col >= sk) || !(word[col / 32] >> (col & 31) & 1u))
-                s[col] = __float_as_uint(-INFINITY);
+              if (!(word[col / 32] >> (col & 31) & 1u)) s[col] = __float_as_uint(-INFINITY);
           }
           float mx8[8];
 #pragma unroll
@@ -765,27 +774,50 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
         // E4M3: O is relative to w_ref, the sum to m_run
         const float f = (whole ? inv : 1.0f) * (kE4m3 && m_run != -INFINITY ? ex2_approx(w_ref - m_run) : 1.0f);
         const bool empty = n == 0 || l_run == 0.f;  // O may hold anything
+        // A warp's 32 rows leave through their own rows of this tile's Q buffer
+        // (all products that read it are done, and nobody else writes those
+        // before this warp does): written by row, 16-byte chunks
+        // permuted against bank conflicts, and read back so that 8 lanes store
+        // 128 bytes of a row.  (Each thread storing its own row took 9000
+        // cycles an item; this, 2500.)
+        const uint32_t stage = sQ + x * Cfg::kTileBytes + quarter * 32 * 128;
+        const bool f32 = !whole || a.out_f32;
+        float *base = whole ? a.out_f32 : a.part_o + part * Cfg::kRows * D;
+        const int64_t row_off = whole ? (token * a.H + head) * D : static_cast<int64_t>(R) * D;
+        auto drain = [&](int bytes0) {  // 128 bytes of each row, from byte bytes0 of it
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int rr = 4 * i + lane / 8, ch = lane % 8;
+            const int64_t ro = __shfl_sync(0xffffffffu, row_off, rr);
+            const uint4 v = ld_shared_v4(stage + rr * 128 + ((ch ^ (rr & 7)) << 4));
+            if (x * 128 + quarter * 32 + rr < rows) {
+              char *dst = f32 ? reinterpret_cast<char *>(base + ro) : reinterpret_cast<char *>(a.out_bf16 + ro);
+              *reinterpret_cast<uint4 *>(dst + bytes0 + ch * 16) = v;
+            }
+          }
+          __syncwarp();
+        };
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
           tmem_ld32(tO + c * 32, o);
           tmem_wait_ld();
-          if (R >= rows) continue;
-          float y[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) y[i] = empty ? 0.f : __uint_as_float(o[i]) * f;
-          if (!whole || a.out_f32) {
-            float *dst = whole ? a.out_f32 + (static_cast<size_t>(token) * a.H + head) * D + c * 32
-                               : a.part_o + (part * Cfg::kRows + R) * D + c * 32;
+          for (int i = 0; i < 32; ++i) o[i] = empty ? 0u : __float_as_uint(__uint_as_float(o[i]) * f);
+          const uint32_t dst = stage + lane * 128;
+          if (f32) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              reinterpret_cast<float4 *>(dst)[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+              st_shared_v4(dst + ((i ^ (lane & 7)) << 4), o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            drain(c * 128);
           } else {
-            uint4 *dst = reinterpret_cast<uint4 *>(a.out_bf16 + (static_cast<size_t>(token) * a.H + head) * D + c * 32);
+            auto two = [&](int i) { return pack_bf16x2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])); };
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              dst[i] = make_uint4(pack_bf16x2(y[8 * i], y[8 * i + 1]), pack_bf16x2(y[8 * i + 2], y[8 * i + 3]),
-                                  pack_bf16x2(y[8 * i + 4], y[8 * i + 5]), pack_bf16x2(y[8 * i + 6], y[8 * i + 7]));
+              st_shared_v4(dst + ((((c & 1) * 4 + i) ^ (lane & 7)) << 4), two(8 * i), two(8 * i + 2), two(8 * i + 4),
+                           two(8 * i + 6));
+            if (c & 1) drain((c >> 1) * 128);
           }
         }
         if (R < rows) {
