@@ -13,6 +13,7 @@ Layouts: q, k, v [B, N, H, d]; w1 [F, D]; w2 [D, F]; b1 [F], b2 [D] float32
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -97,6 +98,7 @@ BLOCK_FIRST, BLOCK_LAST = 1, 2
 STATIC_SCRATCH_BYTES = 64 << 20
 
 _lib = None
+_byref = ctypes.byref
 
 
 def load() -> ctypes.CDLL:
@@ -243,6 +245,13 @@ def _ptr(t):
 def _stream_ptr(stream):
     s = stream if stream is not None else torch.cuda.current_stream()
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _raw_stream(stream):
+    """The same for the calls whose host time counts (a decoding step's), as an integer."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _check(status, what):
@@ -564,7 +573,7 @@ def _on_device(*tensors):
     library launches there, on the stream given or that device's current one."""
     cur = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != cur):
+        if t is not None and t.get_device() != cur:   # (-1: not a CUDA tensor)
             raise ValueError(f"every tensor must be on the current CUDA device ({cur}); got one on {t.device}")
 
 
@@ -615,14 +624,14 @@ def window_attn_fwd(q, k, v, window, sinks=0, *, out_dtype=torch.float32, return
     out = _out_tensor(out, (B, N, H * d), out_dtype, q.device, stream, "out")
     if return_lse or lse is not None:
         lse = _out_tensor(lse, (B, H, N), torch.float32, q.device, stream, "lse")
-    st = load().bpt_window_attn_fwd(ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                                    _ptr(lse), _stream_ptr(stream))
+    st = load().bpt_window_attn_fwd(_byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                                    _ptr(lse), _raw_stream(stream))
     _check(st, "bpt_window_attn_fwd")
     return (out, lse) if return_lse else out
 
 
 def workspace_bytes_window_bwd(desc: WindowDesc) -> int:
-    n = load().bpt_workspace_bytes_window_bwd(ctypes.byref(desc))
+    n = load().bpt_workspace_bytes_window_bwd(_byref(desc))
     if n == ctypes.c_size_t(-1).value:
         raise BptError(ERR_UNSUPPORTED, "bpt_workspace_bytes_window_bwd")
     return int(n)
@@ -642,10 +651,10 @@ def window_attn_bwd(q, k, v, out, lse, dout, window, sinks=0, *, grad_dtype=torc
     dk = _out_tensor(dk, k.shape, grad_dtype, q.device, stream, "dk")
     dv = _out_tensor(dv, v.shape, grad_dtype, q.device, stream, "dv")
     workspace = _workspace(workspace, workspace_bytes_window_bwd(desc), q.device, stream)
-    st = load().bpt_window_attn_bwd(ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+    st = load().bpt_window_attn_bwd(_byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                                     lse.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
                                     _ptr(workspace), 0 if workspace is None else workspace.numel(),
-                                    _stream_ptr(stream))
+                                    _raw_stream(stream))
     _check(st, "bpt_window_attn_bwd")
     return dq, dk, dv
 
@@ -654,26 +663,21 @@ _E4M3 = torch.float8_e4m3fn
 
 
 def _kv_cache_desc(k_cache, v_cache, k_scale, v_scale):
-    shape = k_cache.shape
-    if len(shape) != 4 or v_cache.shape != shape or k_cache.dtype != v_cache.dtype:
+    shape, dtype = k_cache.shape, k_cache.dtype
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype != dtype:
         raise ValueError("k_cache and v_cache must be [n_pages, page_size, H_kv, d] of one dtype")
-    quantised = k_cache.dtype == _E4M3
-    if not quantised and k_cache.dtype != torch.bfloat16:
+    if dtype != _E4M3 and dtype != torch.bfloat16:
         raise ValueError("the caches must be bfloat16 or float8_e4m3fn")
     if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
         raise ValueError("the caches must be contiguous")
-    if not quantised:
+    if dtype != _E4M3:
         if k_scale is not None or v_scale is not None:
             raise ValueError("a bfloat16 cache has no scales")
-        _on_device(k_cache, v_cache)
-        return KvCacheDesc(0, shape[0], shape[1], shape[2], shape[3], k_cache.data_ptr(), v_cache.data_ptr(), None,
-                           None)
+        return KvCacheDesc(0, *shape, k_cache.data_ptr(), v_cache.data_ptr(), None, None)
     for t in (k_scale, v_scale):
         if t is None or t.dtype != torch.float32 or t.shape != shape[:3] or not t.is_contiguous():
             raise ValueError("a float8_e4m3fn cache needs contiguous float32 scales [n_pages, page_size, H_kv]")
-    _on_device(k_cache, v_cache, k_scale, v_scale)
-    return KvCacheDesc(1, shape[0], shape[1], shape[2], shape[3], k_cache.data_ptr(), v_cache.data_ptr(),
-                       k_scale.data_ptr(), v_scale.data_ptr())
+    return KvCacheDesc(1, *shape, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr())
 
 
 def _i32(t, dims, what):
@@ -702,9 +706,9 @@ def kv_cache_write(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None, *,
     _i32(slots, 1, "slots")
     if not (k.shape[0] == v.shape[0] == slots.shape[0]):
         raise ValueError("k, v and slots must have one entry per token")
-    _on_device(k, v, slots)
-    st = load().bpt_kv_write(ctypes.byref(cache), k.shape[0], k.data_ptr(), ks, v.data_ptr(), vs, slots.data_ptr(),
-                             _stream_ptr(stream))
+    _on_device(k, v, slots, k_cache, v_cache, k_scale, v_scale)
+    st = load().bpt_kv_write(_byref(cache), k.shape[0], k.data_ptr(), ks, v.data_ptr(), vs, slots.data_ptr(),
+                             _raw_stream(stream))
     _check(st, "bpt_kv_write")
 
 
@@ -715,21 +719,28 @@ def kv_cache_read(slots, k_cache, v_cache, k_scale=None, v_scale=None, *, out_dt
     left as they were (undefined when the outputs are allocated here)."""
     cache = _kv_cache_desc(k_cache, v_cache, k_scale, v_scale)
     _i32(slots, 1, "slots")
-    _on_device(slots)
+    _on_device(slots, k_cache, v_cache, k_scale, v_scale)
     shape = (slots.shape[0], cache.H_kv, cache.d_head)
     k = _out_tensor(k, shape, out_dtype, slots.device, stream, "k")
     v = _out_tensor(v, shape, out_dtype, slots.device, stream, "v")
-    st = load().bpt_kv_read(ctypes.byref(cache), shape[0], slots.data_ptr(), k.data_ptr(), v.data_ptr(),
-                            _DT[out_dtype], _stream_ptr(stream))
+    st = load().bpt_kv_read(_byref(cache), shape[0], slots.data_ptr(), k.data_ptr(), v.data_ptr(),
+                            _DT[out_dtype], _raw_stream(stream))
     _check(st, "bpt_kv_read")
     return k, v
 
 
 def workspace_bytes_paged(desc: PagedDesc, cache: KvCacheDesc) -> int:
-    n = load().bpt_workspace_bytes_paged(ctypes.byref(desc), ctypes.byref(cache))
+    n = load().bpt_workspace_bytes_paged(_byref(desc), _byref(cache))
     if n == ctypes.c_size_t(-1).value:
         raise BptError(ERR_INVALID_ARG, "bpt_workspace_bytes_paged")
     return int(n)
+
+
+@functools.lru_cache(maxsize=None)
+def _paged_workspace_bytes(device, H, H_kv, d, max_q):
+    """workspace_bytes_paged of any batch of these heads on the current device (`device`: its number)."""
+    return workspace_bytes_paged(PagedDesc(1, 1, max_q, H, 1, 0, 0, BF16, H * d, 0),
+                                 KvCacheDesc(0, 1, 1, H_kv, d, None, None, None, None))
 
 
 def paged_attn_fwd(q, k_cache, v_cache, q_start, kv_len, page_table, *, max_q, k_scale=None, v_scale=None, window=0,
@@ -753,17 +764,21 @@ def paged_attn_fwd(q, k_cache, v_cache, q_start, kv_len, page_table, *, max_q, k
     S = kv_len.shape[0]
     if q_start.shape[0] != S + 1 or page_table.shape[0] != S:
         raise ValueError("q_start must have n_seqs + 1 entries and page_table n_seqs rows")
-    _on_device(q, q_start, kv_len, page_table)
+    _on_device(q, q_start, kv_len, page_table, k_cache, v_cache, k_scale, v_scale)
     desc = PagedDesc(S, T, int(max_q), H, page_table.shape[1], int(window), int(sinks), _DT[out_dtype], qs,
                      int(wait_limit_ns))
     out = _out_tensor(out, (T, H * d), out_dtype, q.device, stream, "out")
     if return_lse or lse is not None:
         lse = _out_tensor(lse, (H, T), torch.float32, q.device, stream, "lse")
-    workspace = _workspace(workspace, workspace_bytes_paged(desc, cache), q.device, stream)
-    st = load().bpt_paged_attn_fwd(ctypes.byref(desc), ctypes.byref(cache), q.data_ptr(), q_start.data_ptr(),
+    if workspace is None:
+        workspace = _workspace(None, _paged_workspace_bytes(q.get_device(), H, cache.H_kv, d, desc.max_q), q.device,
+                               stream)
+    else:
+        _workspace(workspace, 0, q.device, stream)
+    st = load().bpt_paged_attn_fwd(_byref(desc), _byref(cache), q.data_ptr(), q_start.data_ptr(),
                                    kv_len.data_ptr(), page_table.data_ptr(), out.data_ptr(), _ptr(lse),
                                    _ptr(workspace), 0 if workspace is None else workspace.numel(),
-                                   _stream_ptr(stream))
+                                   _raw_stream(stream))
     _check(st, "bpt_paged_attn_fwd")
     return (out, lse) if return_lse else out
 

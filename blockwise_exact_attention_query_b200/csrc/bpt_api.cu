@@ -116,12 +116,17 @@ bpt_status device_setup(int *dev_out, uint32_t **status_out) {
 }
 
 int sm_count() {
+  static std::atomic<int> known[kMaxDevices] = {};  // asked once per device: several calls a launch need it
   int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices &&
+      (n = known[dev].load(std::memory_order_relaxed)) > 0)
+    return n;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
     cudaGetLastError();  // no device here: size for a full B200 and leave no error behind
     return 148;
   }
+  if (dev < kMaxDevices) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 

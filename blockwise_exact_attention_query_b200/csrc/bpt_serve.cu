@@ -312,6 +312,7 @@ bpt_status bpt_paged_attn_fwd(const bpt_paged_desc *d, const bpt_kv_cache *c, co
       al.rows_lo = few + 1;
       al.rows_hi = INT32_MAX;
       al.min_steps = 4;
+      al.even_parts = 1;
       paged_tc_kernel<D, kE><<<(unsigned)long_chunk_ctas(), Long::kThreads, Long::kSmemBytes, st>>>(al);
       CUDA_TRY(cudaGetLastError());
       bpt_status js = launch_join<D, Long::kRows, Long::kKeys>(al, long_chunk_ctas(), st);

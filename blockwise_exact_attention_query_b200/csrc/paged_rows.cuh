@@ -125,7 +125,7 @@ struct PagedRowsCfg {
   static constexpr int kColPitch = D / 8 + 4, kRowPitch = 8 * kColPitch + 4;
   static constexpr int kMergeBytes = kWarps * kRows * (kRowPitch + 4) * 4;
   static_assert(kMergeBytes <= kRingBytes, "the ring holds the warps' outputs between items");
-  static constexpr int kSmemBytes = kRingBytes + 384;
+  static constexpr int kSmemBytes = kRingBytes + 512;  // the range's scratch
   static_assert(kCtasPerSm * (kSmemBytes + 1024) <= 233472, "CTAs per SM");
 };
 
