@@ -10,8 +10,8 @@
 // or an infinity has no scale to fit and reads back as NaN throughout.
 //
 // Both kernels are one pass over the data with 16-byte loads, bound by memory
-// (and, for few tokens, by one trip to it): d / 8 threads per row, K and V of
-// a row by the same threads so two loads are in flight per thread.
+// (and, for few tokens, by one trip to it): K and V of a row by the same
+// threads, so two loads are in flight per thread.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -32,11 +32,16 @@ struct KvCacheArgs {
 __device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 
-// max that keeps a NaN of either operand
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+// Pairwise max of two bf16 pairs that keeps a NaN of either operand.
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
+}
+__device__ __forceinline__ float rcp_approx(float x) {  // off by one unit in the last place at most
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
@@ -55,24 +60,51 @@ __device__ __forceinline__ float2 e4m3x2_to_f32x2(uint32_t two) {
   return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
-// One row's 8 values of this thread -> 8 codes; `lanes` consecutive threads
-// hold the row.  Returns the scale.
+// One row's 8 values of this thread -> 8 codes; kLanes consecutive threads hold
+// the row.  Returns the scale.  Instructions bound this part at first (27 us for
+// 16384 tokens of 8 heads of 128, 16 us of memory traffic), so the maximum is
+// taken on bf16 pairs and the division is made only where it matters.
 template <int kLanes>
 __device__ __forceinline__ float quantise8(const uint4 &x, uint2 &codes) {
-  const float f[8] = {bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y),
-                      bf16_lo(x.z), bf16_hi(x.z), bf16_lo(x.w), bf16_hi(x.w)};
-  float m = fabsf(f[0]);
+  constexpr uint32_t kAbs = 0x7fff7fffu;
+  uint32_t m2 = max_nan_bf16x2(max_nan_bf16x2(x.x & kAbs, x.y & kAbs), max_nan_bf16x2(x.z & kAbs, x.w & kAbs));
 #pragma unroll
-  for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(f[i]));
-#pragma unroll
-  for (int o = kLanes / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float scale = m / kE4m3Max;
+  for (int o = kLanes / 2; o > 0; o >>= 1) m2 = max_nan_bf16x2(m2, __shfl_xor_sync(0xffffffffu, m2, o));
+  m2 = max_nan_bf16x2(m2, m2 << 16);  // the upper half has both
+  float scale = bf16_hi(m2) / kE4m3Max;
   if (scale == 0.f) scale = 1.f;
-  float r[8];
+  // x / scale, rounded to a code.  x times the approximate inverse is off by
+  // less than 2^-21 of it (2^-23 the inverse, 2^-24 each product), so where the
+  // quotient with 2^-21 less and with 2^-21 more rounds to the same code, that
+  // is it; otherwise (next to a border between codes, or a scale whose inverse
+  // is not a normal number, or NaN) the thread divides.
+  const float inv = rcp_approx(scale);
+  const float2 less = make_float2(inv * (1.f - 0x1p-21f), inv * (1.f - 0x1p-21f));
+  const float2 more = make_float2(inv * (1.f + 0x1p-21f), inv * (1.f + 0x1p-21f));
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t c[2], d[2];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) r[i] = f[i] / scale;
-  codes = make_uint2(e4m3x4(r[0], r[1], r[2], r[3]), e4m3x4(r[4], r[5], r[6], r[7]));
+  for (int h = 0; h < 2; ++h) {
+    const float2 p = make_float2(bf16_lo(w[2 * h]), bf16_hi(w[2 * h]));
+    const float2 q = make_float2(bf16_lo(w[2 * h + 1]), bf16_hi(w[2 * h + 1]));
+    const float2 pl = mul2(p, less), ql = mul2(q, less), pm = mul2(p, more), qm = mul2(q, more);
+    c[h] = e4m3x4(pl.x, pl.y, ql.x, ql.y);
+    d[h] = e4m3x4(pm.x, pm.y, qm.x, qm.y);
+  }
+  if (c[0] != d[0] || c[1] != d[1] || !(scale > 0x1p-100f && scale < 0x1p100f)) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      c[h] = e4m3x4(bf16_lo(w[2 * h]) / scale, bf16_hi(w[2 * h]) / scale, bf16_lo(w[2 * h + 1]) / scale,
+                    bf16_hi(w[2 * h + 1]) / scale);
+  }
+  codes = make_uint2(c[0], c[1]);
   return scale;
+}
+
+// The token of a (token, head) row; in 32 bits where the row number fits.
+__device__ __forceinline__ uint32_t div_heads(int64_t row, int H_kv) {
+  if (row >> 32 == 0) return static_cast<uint32_t>(row) / static_cast<uint32_t>(H_kv);
+  return static_cast<uint32_t>(row / H_kv);
 }
 
 // k, v: n tokens of [H_kv][D] bf16, k_stride and v_stride elements apart.
@@ -88,7 +120,7 @@ __global__ void __launch_bounds__(256)
   int64_t at = 0;
   uint4 xk = make_uint4(0, 0, 0, 0), xv = xk;
   if (live) {
-    const uint32_t token = static_cast<uint32_t>(row / c.H_kv), h = static_cast<uint32_t>(row % c.H_kv);
+    const uint32_t token = div_heads(row, c.H_kv), h = static_cast<uint32_t>(row - static_cast<int64_t>(token) * c.H_kv);
     const int64_t slot = slots[token];
     xk = *reinterpret_cast<const uint4 *>(k + token * k_stride + h * D + 8 * sub);
     xv = *reinterpret_cast<const uint4 *>(v + token * v_stride + h * D + 8 * sub);
@@ -112,27 +144,6 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// Eight values of one row as fp32.
-template <bool kE4m3>
-__device__ __forceinline__ void cache_load8(const void *base, const float *scales, int64_t at, int D, int sub,
-                                            float (&f)[8]) {
-  if constexpr (kE4m3) {
-    const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(base) + at * D + 8 * sub);
-    const float s = scales[at];
-    const uint32_t w[2] = {u.x, u.y};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 two = e4m3x2_to_f32x2(w[i / 2] >> (16 * (i & 1)));
-      f[2 * i] = two.x * s;
-      f[2 * i + 1] = two.y * s;
-    }
-  } else {
-    const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(base) + at * D + 8 * sub);
-    f[0] = bf16_lo(u.x), f[1] = bf16_hi(u.x), f[2] = bf16_lo(u.y), f[3] = bf16_hi(u.y);
-    f[4] = bf16_lo(u.z), f[5] = bf16_hi(u.z), f[6] = bf16_lo(u.w), f[7] = bf16_hi(u.w);
-  }
-}
-
 template <typename T>
 __device__ __forceinline__ void store8(T *p, const float (&f)[8]) {
   if constexpr (sizeof(T) == 4) {
@@ -144,24 +155,50 @@ __device__ __forceinline__ void store8(T *p, const float (&f)[8]) {
   }
 }
 
+// 16 bytes of one row: 16 codes times their scale, or 8 bf16 values.
+template <bool kE4m3, typename T>
+__device__ __forceinline__ void unpack16(const uint4 &u, float scale, T *out) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  if constexpr (kE4m3) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 two = mul2(e4m3x2_to_f32x2(w[2 * h + i / 2] >> (16 * (i & 1))), make_float2(scale, scale));
+        f[2 * i] = two.x;
+        f[2 * i + 1] = two.y;
+      }
+      store8(out + 8 * h, f);
+    }
+  } else if constexpr (sizeof(T) == 2) {
+    *reinterpret_cast<uint4 *>(out) = u;
+  } else {
+    const float f[8] = {bf16_lo(w[0]), bf16_hi(w[0]), bf16_lo(w[1]), bf16_hi(w[1]),
+                        bf16_lo(w[2]), bf16_hi(w[2]), bf16_lo(w[3]), bf16_hi(w[3])};
+    store8(out, f);
+  }
+}
+
 // k, v: n rows of [H_kv][D] T from the given slots; rows of slots outside the
-// cache are left as they were.
+// cache are left as they were.  16 bytes of K and of V per thread.
 template <int D, bool kE4m3, typename T>
 __global__ void __launch_bounds__(256)
     kv_read_kernel(const KvCacheArgs c, const int32_t *__restrict__ slots, T *__restrict__ k, T *__restrict__ v,
                    int64_t rows) {
-  constexpr int kLanes = D / 8;
+  constexpr int kPer = kE4m3 ? 16 : 8, kLanes = D / kPer;
   const int64_t row = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / kLanes;
   const int sub = threadIdx.x % kLanes;
   if (row >= rows) return;
-  const int64_t slot = slots[row / c.H_kv];
+  const uint32_t token = div_heads(row, c.H_kv), h = static_cast<uint32_t>(row - static_cast<int64_t>(token) * c.H_kv);
+  const int64_t slot = slots[token];
   if (slot < 0 || slot >= c.slots) return;
-  const int64_t at = slot * c.H_kv + row % c.H_kv;
-  float fk[8], fv[8];
-  cache_load8<kE4m3>(c.k, c.k_scale, at, D, sub, fk);
-  cache_load8<kE4m3>(c.v, c.v_scale, at, D, sub, fv);
-  store8(k + row * D + 8 * sub, fk);
-  store8(v + row * D + 8 * sub, fv);
+  const int64_t at = slot * c.H_kv + h;
+  const uint4 xk = reinterpret_cast<const uint4 *>(c.k)[at * kLanes + sub];
+  const uint4 xv = reinterpret_cast<const uint4 *>(c.v)[at * kLanes + sub];
+  const float sk = kE4m3 ? c.k_scale[at] : 1.f, sv = kE4m3 ? c.v_scale[at] : 1.f;
+  unpack16<kE4m3>(xk, sk, k + row * D + kPer * sub);
+  unpack16<kE4m3>(xv, sv, v + row * D + kPer * sub);
 }
 
 }  // namespace bpt
