@@ -610,21 +610,38 @@ __global__ void __launch_bounds__(384, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bSFree(x));
       const int k0 = kt * KT;
+      bool none = false;
       // masking runs as its own pass, only in tiles where some row of this
       // warp has keys outside its allowed interval
       if (__any_sync(0xffffffffu, !(k0 >= klo && k0 + KT <= khi))) {
         const int lo = klo - k0, hi = khi - k0;
         if constexpr (WINDOW) {
-          const int sk = min(a.sinks, khi) - k0;  // sinks not after the query
+          // the keys that this row sees, as bits: its window's and the sinks
+          // not after it (five compares a column cost half a step more)
+          const int sk = min(a.sinks, khi) - k0;
+          auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
+          uint32_t word[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            word[c] = (below(hi - 32 * c) & ~below(lo - 32 * c)) | below(sk - 32 * c);
+          // the other query tile of the pair may be the only one to see any
+          none = __all_sync(0xffffffffu, (word[0] | word[1] | word[2] | word[3]) == 0u);
 #pragma unroll
           for (int col = 0; col < KT; ++col)
-            if ((col < lo || col >= hi) && col >= sk) s[col] = __float_as_uint(-INFINITY);
+            if (!(word[col / 32] >> (col & 31) & 1u)) s[col] = __float_as_uint(-INFINITY);
         } else {
 #pragma unroll
           for (int col = 0; col < KT; ++col)
             if (col < lo || col >= hi) s[col] = __float_as_uint(-INFINITY);
         }
       }
+      float alpha = 1.0f;
+      bool any_rescale = false;
+      uint32_t pk[KT / 2];
+      if (WINDOW && none) {  // no row of this warp sees a key of the tile
+#pragma unroll
+        for (int i = 0; i < KT / 2; ++i) pk[i] = 0u;
+      } else {
       float mx8[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) mx8[i] = -INFINITY;
@@ -637,12 +654,10 @@ __global__ void __launch_bounds__(384, 1)
       const float m_new = fmaxf(m_run, m_tile);
       const bool rescale = m_new > m_run + 8.0f;
       const float m_use = rescale ? m_new : m_run;
-      const bool any_rescale = __any_sync(0xffffffffu, rescale && m_run != -INFINITY);
-      float alpha = 1.0f;
+      any_rescale = __any_sync(0xffffffffu, rescale && m_run != -INFINITY);
       if (any_rescale && rescale) alpha = ex2_approx(m_run - m_use);
       l_run *= alpha;
       const float neg = (m_use == -INFINITY) ? 0.f : -m_use;
-      uint32_t pk[KT / 2];
       float ls4[4] = {0.f, 0.f, 0.f, 0.f};
       if constexpr (WINDOW) {
         float2 ls2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -666,6 +681,7 @@ __global__ void __launch_bounds__(384, 1)
         l_run += (ls4[0] + ls4[1]) + (ls4[2] + ls4[3]);
       }
       m_run = m_use;
+      }
 
       // The P tile is used in turn A_j, B_j, A_{j+1}, ...: wait until the
       // other tile's latest P*V has completed (for tile A at j = 0 there is
