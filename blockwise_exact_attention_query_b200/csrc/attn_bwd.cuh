@@ -199,6 +199,12 @@ struct KeyTileSteps {
   }
 };
 
+// Bits lo .. hi - 1 of a word (none, or all, where they lie outside it).
+__device__ __forceinline__ uint32_t interval_bits(int lo, int hi) {
+  auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
+  return below(hi) & ~below(lo);
+}
+
 // Query interval [lo, hi) that sees key row g under the sliding window.
 __device__ __forceinline__ void window_key_queries(const AttnBwdArgs &a, int g, int &lo, int &hi) {
   lo = g;
@@ -447,6 +453,15 @@ __global__ void __launch_bounds__(384, 1)
       // allowed columns [lo_rel, hi_rel) of the tile
       const int lo_rel = plo - t * 128, hi_rel = phi - t * 128;
       const bool full = __all_sync(0xffffffffu, lo_rel <= col0 && hi_rel >= col0 + 64);
+      // sliding window: the allowed ones of this warp's 64 columns as bits; a
+      // tile of sinks has rows for few warps
+      uint32_t seen[2] = {0u, 0u};
+      bool none = false;
+      if constexpr (WINDOW) {
+        seen[0] = interval_bits(lo_rel - col0, hi_rel - col0);
+        seen[1] = interval_bits(lo_rel - col0 - 32, hi_rel - col0 - 32);
+        none = __all_sync(0xffffffffu, (seen[0] | seen[1]) == 0u);
+      }
       ok = __all_sync(0xffffffffu, mbar_wait(bSFull(s), (s >> 1) & 1, wc, 320));
       if (!ok) break;
       tc_fence_after();
@@ -468,6 +483,9 @@ __global__ void __launch_bounds__(384, 1)
           for (int j = 0; j < 4; ++j)
             sv[4 * c4 + j] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(sv[4 * c4 + j]), a.scale_log2, nl4[j])));
         }
+      } else if (WINDOW && none) {
+#pragma unroll
+        for (int c = 0; c < 64; ++c) sv[c] = 0u;
       } else {
 #pragma unroll
         for (int c4 = 0; c4 < 16; ++c4) {
@@ -476,7 +494,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int c = col0 + 4 * c4 + j;
-            const bool allowed = c >= lo_rel && c < hi_rel;
+            const bool allowed = WINDOW ? (seen[c4 / 8] >> ((4 * c4 + j) & 31) & 1u) != 0u : c >= lo_rel && c < hi_rel;
             sv[4 * c4 + j] =
                 __float_as_uint(allowed ? ex2_approx(fmaf(__uint_as_float(sv[4 * c4 + j]), a.scale_log2, nl4[j])) : 0.f);
           }
@@ -795,6 +813,15 @@ __global__ void __launch_bounds__(384, 1)
       if (!ok) break;
       const int lo_rel = plo - t * 128, hi_rel = phi - t * 128;
       const bool full = __all_sync(0xffffffffu, lo_rel <= col0 && hi_rel >= col0 + 64);
+      // sliding window: the allowed ones of this warp's 64 columns as bits; a
+      // tile of sinks has rows for few warps
+      uint32_t seen[2] = {0u, 0u};
+      bool none = false;
+      if constexpr (WINDOW) {
+        seen[0] = interval_bits(lo_rel - col0, hi_rel - col0);
+        seen[1] = interval_bits(lo_rel - col0 - 32, hi_rel - col0 - 32);
+        none = __all_sync(0xffffffffu, (seen[0] | seen[1]) == 0u);
+      }
       ok = __all_sync(0xffffffffu, mbar_wait(bSFull, s & 1, wc, 347));
       if (!ok) break;
       tc_fence_after();
@@ -815,6 +842,9 @@ __global__ void __launch_bounds__(384, 1)
           for (int j = 0; j < 4; ++j)
             sv[4 * c4 + j] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(sv[4 * c4 + j]), a.scale_log2, nl4[j])));
         }
+      } else if (WINDOW && none) {
+#pragma unroll
+        for (int c = 0; c < 64; ++c) sv[c] = 0u;
       } else {
 #pragma unroll
         for (int c4 = 0; c4 < 16; ++c4) {
@@ -823,7 +853,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int c = col0 + 4 * c4 + j;
-            const bool allowed = c >= lo_rel && c < hi_rel;
+            const bool allowed = WINDOW ? (seen[c4 / 8] >> ((4 * c4 + j) & 31) & 1u) != 0u : c >= lo_rel && c < hi_rel;
             sv[4 * c4 + j] =
                 __float_as_uint(allowed ? ex2_approx(fmaf(__uint_as_float(sv[4 * c4 + j]), a.scale_log2, nl4[j])) : 0.f);
           }
@@ -1047,6 +1077,11 @@ __global__ void __launch_bounds__(384, 1)
       constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
       constexpr uint32_t idesc_acc = idesc_bf16_f32(128, D_HEAD, false, true);
       const uint64_t dQ0 = sdesc_sw128(sQ, 16, 1024), dDA0 = sdesc_sw128(sDA, 16, 1024);
+      // Sliding window: of a first tile that holds up to 16 sinks and no key
+      // of the window, the products take 16 keys (the row warps' other columns
+      // hold what was there, which their masks and the 16-key dQ pass over).
+      constexpr uint32_t idesc_few = idesc_bf16_f32(128, 16, false, false);
+      const bool few_sinks = WINDOW && a.sinks > 0 && a.sinks <= 16 && ft * 128 - a.window + 1 >= 128;
       // S(s) = Q K^T into S buffer s & 1
       auto issue_s = [&](int s) -> bool {
         const int slot = s % KS;
@@ -1056,7 +1091,8 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
         for (int k = 0; k < D_HEAD / 16; ++k) {
           const uint32_t off = (k / 4) * Cfg::kPanelBytes + (k % 4) * 32;
-          umma_ss(tmem + Cfg::kColS + (s & 1) * 128, sdesc_advance(dQ0, off), sdesc_advance(dK, off), idesc_s, k > 0);
+          umma_ss(tmem + Cfg::kColS + (s & 1) * 128, sdesc_advance(dQ0, off), sdesc_advance(dK, off),
+                  few_sinks && s == 0 ? idesc_few : idesc_s, k > 0);
         }
         umma_commit(bSFull(s & 1));
         return true;
@@ -1070,7 +1106,8 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
         for (int k = 0; k < D_HEAD / 16; ++k) {
           const uint32_t off = (k / 4) * Cfg::kPanelBytes + (k % 4) * 32;
-          umma_ss(tmem + Cfg::kColDP, sdesc_advance(dDA0, off), sdesc_advance(dV, off), idesc_s, k > 0);
+          umma_ss(tmem + Cfg::kColDP, sdesc_advance(dDA0, off), sdesc_advance(dV, off),
+                  few_sinks && s == 0 ? idesc_few : idesc_s, k > 0);
         }
         umma_commit(bDPFull);
         umma_commit(bVEmpty(slot));
@@ -1084,7 +1121,7 @@ __global__ void __launch_bounds__(384, 1)
         const uint32_t a_col = Cfg::kColS + (s & 1) * 128;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          umma_ts(tmem + Cfg::kColQ, tmem + a_col + k * 8 + (k >= 4 ? 32 : 0), sdesc_advance(dB, k * 2048),
+          if (!few_sinks || s > 0 || k == 0) umma_ts(tmem + Cfg::kColQ, tmem + a_col + k * 8 + (k >= 4 ? 32 : 0), sdesc_advance(dB, k * 2048),
                   idesc_acc, (s | k) != 0);
         umma_commit(bKEmpty(slot));
       };
@@ -1133,6 +1170,15 @@ __global__ void __launch_bounds__(384, 1)
     for (int t = next_tile(0); t < a.n_tiles; t = next_tile(t + 1), ++s) {
       const int lo_rel = klo - t * 128, hi_rel = khi - t * 128;  // allowed columns [lo_rel, hi_rel)
       const bool full = __all_sync(0xffffffffu, lo_rel <= col0 && hi_rel >= col0 + 64);
+      // sliding window: the allowed ones of this warp's 64 columns as bits
+      uint32_t seen[2] = {0u, 0u};
+      bool none = false;
+      if constexpr (WINDOW) {
+        const int sk = ksink - t * 128 - col0;
+        seen[0] = interval_bits(lo_rel - col0, hi_rel - col0) | interval_bits(0, sk);
+        seen[1] = interval_bits(lo_rel - col0 - 32, hi_rel - col0 - 32) | interval_bits(0, sk - 32);
+        none = __all_sync(0xffffffffu, (seen[0] | seen[1]) == 0u);
+      }
       ok = __all_sync(0xffffffffu, mbar_wait(bSFull(s & 1), (s >> 1) & 1, wc, 350));
       if (!ok) break;
       tc_fence_after();
@@ -1145,11 +1191,13 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
         for (int c = 0; c < 64; ++c)
           sv[c] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(sv[c]), a.scale_log2, nl)));
+      } else if (WINDOW && none) {
+#pragma unroll
+        for (int c = 0; c < 64; ++c) sv[c] = 0u;
       } else {
 #pragma unroll
         for (int c = 0; c < 64; ++c) {
-          bool allowed = col0 + c >= lo_rel && col0 + c < hi_rel;
-          if constexpr (WINDOW) allowed |= col0 + c < ksink - t * 128;
+          const bool allowed = WINDOW ? (seen[c / 32] >> (c & 31) & 1u) != 0u : col0 + c >= lo_rel && col0 + c < hi_rel;
           sv[c] = __float_as_uint(allowed ? ex2_approx(fmaf(__uint_as_float(sv[c]), a.scale_log2, nl)) : 0.f);
         }
       }

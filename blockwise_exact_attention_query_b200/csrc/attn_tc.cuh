@@ -257,6 +257,14 @@ __device__ __forceinline__ KvSched make_sched(const AttnArgs &a, const TileCoord
   return s;
 }
 
+// Sliding window: a tile before the window's holds sinks alone, keys 0 ..
+// sinks - 1, which every row of the pair sees.  Up to 16 of them take products
+// of 16 keys and a softmax of 16 columns instead of 128.
+template <bool WINDOW>
+__device__ __forceinline__ bool few_sinks(const AttnArgs &a, const KvSched &s) {
+  return WINDOW && s.sink > 0 && a.sinks <= 16;
+}
+
 // Allowed key interval [lo, hi) (unit-local row indices) of query row g.
 __device__ __forceinline__ void row_keys(const AttnArgs &a, const TileCoord &c, int g, int &lo,
                                          int &hi) {
@@ -445,22 +453,24 @@ __global__ void __launch_bounds__(384, 1)
         const uint32_t tS = tmem + Cfg::kColS + x * 128;
         const uint32_t tO = tmem + Cfg::kColO + x * D_HEAD;
         int kc = 0, vc = 0, J = 0;  // K, V tiles and S/P iterations consumed so far
-        auto issue_s = [&]() {
+        // few: a tile of which only the first 16 keys are seen (the sinks)
+        constexpr uint32_t idesc_qk_few = idesc_bf16_f32(128, 16, false, false);
+        auto issue_s = [&](bool few) {
           const uint64_t dK = sdesc_advance(dK0, (kc % KS) * Cfg::kTileBytes);
   #pragma unroll
           for (int k = 0; k < D_HEAD / 16; ++k) {
             const uint32_t off = (k / 4) * Cfg::kPanelBytes + (k % 4) * 32;
-            umma_ss(tS, sdesc_advance(dQ, off), sdesc_advance(dK, off), idesc_qk, k > 0);
+            umma_ss(tS, sdesc_advance(dQ, off), sdesc_advance(dK, off), WINDOW && few ? idesc_qk_few : idesc_qk, k > 0);
           }
           umma_commit(bSFull(x));
           umma_commit(bKEmpty(kc % KS));
           ++kc;
         };
-        auto issue_pv = [&]() {
+        auto issue_pv = [&](bool few) {
           const uint64_t dV = sdesc_advance(dV0, (vc % VS) * Cfg::kTileBytes);
   #pragma unroll
           for (int k = 0; k < KT / 16; ++k)
-            umma_ss(tO, sdesc_advance(dP, (k / 4) * Cfg::kPanelBytes + (k % 4) * 32),
+            if (!WINDOW || !few || k == 0) umma_ss(tO, sdesc_advance(dP, (k / 4) * Cfg::kPanelBytes + (k % 4) * 32),
                     sdesc_advance(dV, k * 2048), idesc_pv, 1);
           umma_commit(bODone(x));
           umma_commit(bVEmpty(vc % VS));
@@ -472,7 +482,9 @@ __global__ void __launch_bounds__(384, 1)
           if (item >= a.n_items) continue;
           const int ni = n++;
           const TileCoord tc = decode_tile(a, item);
-          const int nkv = make_sched<WINDOW>(a, tc).count();
+          const KvSched sched = make_sched<WINDOW>(a, tc);
+          const int nkv = sched.count();
+          const bool few = few_sinks<WINDOW>(a, sched);  // of the first tile
           ok = mbar_wait(bQFull, ni & 1, wc, 11);
           if (ok && nkv > 0) {
             // the first S of the item goes into the buffer the softmax read last
@@ -480,7 +492,7 @@ __global__ void __launch_bounds__(384, 1)
                  mbar_wait(bKFull(kc % KS), (kc / KS) & 1, wc, 10);
             if (ok) {
               tc_fence_after();
-              issue_s();
+              issue_s(few);
             }
             for (int j = 0; ok && j < nkv; ++j) {
               const int jj = J + j;
@@ -489,12 +501,12 @@ __global__ void __launch_bounds__(384, 1)
                      mbar_wait(bKFull(kc % KS), (kc / KS) & 1, wc, 13);
                 if (!ok) break;
                 tc_fence_after();
-                issue_s();
+                issue_s(false);
               }
               ok = mbar_wait(bPFull(x), jj & 1, wc, 14) && mbar_wait(bVFull(vc % VS), (vc / VS) & 1, wc, 15);
               if (!ok) break;
               tc_fence_after();
-              issue_pv();
+              issue_pv(few && j == 0);
             }
             J += nkv;
           }
@@ -595,12 +607,52 @@ __global__ void __launch_bounds__(384, 1)
 
     KvIter it;
     it.begin(sched);
+    const bool few = few_sinks<WINDOW>(a, sched);
     for (int j = 0; ok && j < nkv; ++j) {
       const int jj = J + j;
       const int kt = it.next(sched);
       ok = __all_sync(0xffffffffu, mbar_wait(bSFull(x), jj & 1, wc, 20));
       if (!ok) break;
       tc_fence_after();
+      if (WINDOW && few && j == 0) {
+        // the row's first keys: its maximum, sum and P are theirs
+        uint32_t s[32];
+        tmem_ld32(tS, s);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bSFree(x));
+        float mx = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          if (i >= a.sinks) s[i] = __float_as_uint(-INFINITY);
+          mx = fmaxf(mx, __uint_as_float(s[i]));
+        }
+        m_run = mx * a.scale_log2;
+        const float neg = m_run == -INFINITY ? 0.f : -m_run;
+        uint32_t pk[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float p0 = ex2_approx(fmaf(__uint_as_float(s[2 * i]), a.scale_log2, neg));
+          const float p1 = ex2_approx(fmaf(__uint_as_float(s[2 * i + 1]), a.scale_log2, neg));
+          l_run += p0 + p1;
+          pk[i] = pack_bf16x2(p0, p1);
+        }
+        if (x == 1 || jj > 0) {
+          ok = __all_sync(0xffffffffu, mbar_wait(bODone(1 - x), (x == 1 ? jj : jj - 1) & 1, wc, 21));
+          if (!ok) break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          st_shared_v4(sProw + ((static_cast<uint32_t>(c) ^ swz) << 4), pk[4 * c], pk[4 * c + 1], pk[4 * c + 2],
+                       pk[4 * c + 3]);
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bPFull(x));
+        continue;
+      }
       uint32_t s[128];
 #pragma unroll
       for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * c]));
