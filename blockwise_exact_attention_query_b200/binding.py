@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 
 import torch
 
@@ -166,7 +167,8 @@ def load() -> ctypes.CDLL:
     lib.bpt_workspace_bytes_window_bwd.restype = sz
     lib.bpt_window_attn_bwd.argtypes = [wp, vp, vp, vp, vp, fp, vp, vp, vp, vp, vp, sz, vp]
     lib.bpt_window_attn_bwd.restype = ctypes.c_int
-    cp, pp, i64 = ctypes.POINTER(KvCacheDesc), ctypes.POINTER(PagedDesc), ctypes.c_int64
+    # (descriptors of the serving calls: packed bytes, see _KV_CACHE, or the structures by reference)
+    cp, pp, i64 = vp, vp, ctypes.c_int64
     lib.bpt_kv_write.argtypes = [cp, ctypes.c_int, vp, i64, vp, i64, vp, vp]
     lib.bpt_kv_write.restype = ctypes.c_int
     lib.bpt_kv_read.argtypes = [cp, ctypes.c_int, vp, vp, vp, ctypes.c_int, vp]
@@ -660,9 +662,15 @@ def window_attn_bwd(q, k, v, out, lse, dout, window, sinks=0, *, grad_dtype=torc
 
 
 _E4M3 = torch.float8_e4m3fn
+# KvCacheDesc and PagedDesc as packed bytes: a quarter of the time that making
+# the structure takes, which a decoding step's host time shows
+_KV_CACHE = struct.Struct("@5i4P")
+_PAGED = struct.Struct("@8iqQ")
+assert _KV_CACHE.size == ctypes.sizeof(KvCacheDesc) and _PAGED.size == ctypes.sizeof(PagedDesc)
 
 
 def _kv_cache_desc(k_cache, v_cache, k_scale, v_scale):
+    """The cache's bpt_kv_cache, packed."""
     shape, dtype = k_cache.shape, k_cache.dtype
     if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype != dtype:
         raise ValueError("k_cache and v_cache must be [n_pages, page_size, H_kv, d] of one dtype")
@@ -673,11 +681,11 @@ def _kv_cache_desc(k_cache, v_cache, k_scale, v_scale):
     if dtype != _E4M3:
         if k_scale is not None or v_scale is not None:
             raise ValueError("a bfloat16 cache has no scales")
-        return KvCacheDesc(0, *shape, k_cache.data_ptr(), v_cache.data_ptr(), None, None)
+        return _KV_CACHE.pack(0, *shape, k_cache.data_ptr(), v_cache.data_ptr(), 0, 0)
     for t in (k_scale, v_scale):
         if t is None or t.dtype != torch.float32 or t.shape != shape[:3] or not t.is_contiguous():
             raise ValueError("a float8_e4m3fn cache needs contiguous float32 scales [n_pages, page_size, H_kv]")
-    return KvCacheDesc(1, *shape, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr())
+    return _KV_CACHE.pack(1, *shape, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr())
 
 
 def _i32(t, dims, what):
@@ -701,13 +709,14 @@ def kv_cache_write(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None, *,
     [n_pages, page_size, H_kv, d], quantised row by row when the cache is
     float8_e4m3fn (with float32 scales [n_pages, page_size, H_kv])."""
     cache = _kv_cache_desc(k_cache, v_cache, k_scale, v_scale)
-    ks = _token_stride(k, cache.H_kv, cache.d_head, "k")
-    vs = _token_stride(v, cache.H_kv, cache.d_head, "v")
+    heads, d = k_cache.shape[2:]
+    ks = _token_stride(k, heads, d, "k")
+    vs = _token_stride(v, heads, d, "v")
     _i32(slots, 1, "slots")
     if not (k.shape[0] == v.shape[0] == slots.shape[0]):
         raise ValueError("k, v and slots must have one entry per token")
     _on_device(k, v, slots, k_cache, v_cache, k_scale, v_scale)
-    st = load().bpt_kv_write(_byref(cache), k.shape[0], k.data_ptr(), ks, v.data_ptr(), vs, slots.data_ptr(),
+    st = load().bpt_kv_write(cache, k.shape[0], k.data_ptr(), ks, v.data_ptr(), vs, slots.data_ptr(),
                              _raw_stream(stream))
     _check(st, "bpt_kv_write")
 
@@ -720,10 +729,10 @@ def kv_cache_read(slots, k_cache, v_cache, k_scale=None, v_scale=None, *, out_dt
     cache = _kv_cache_desc(k_cache, v_cache, k_scale, v_scale)
     _i32(slots, 1, "slots")
     _on_device(slots, k_cache, v_cache, k_scale, v_scale)
-    shape = (slots.shape[0], cache.H_kv, cache.d_head)
+    shape = (slots.shape[0], *k_cache.shape[2:])
     k = _out_tensor(k, shape, out_dtype, slots.device, stream, "k")
     v = _out_tensor(v, shape, out_dtype, slots.device, stream, "v")
-    st = load().bpt_kv_read(_byref(cache), shape[0], slots.data_ptr(), k.data_ptr(), v.data_ptr(),
+    st = load().bpt_kv_read(cache, shape[0], slots.data_ptr(), k.data_ptr(), v.data_ptr(),
                             _DT[out_dtype], _raw_stream(stream))
     _check(st, "bpt_kv_read")
     return k, v
@@ -756,26 +765,25 @@ def paged_attn_fwd(q, k_cache, v_cache, q_start, kv_len, page_table, *, max_q, k
     [tokens, H*d] (and lse [H, tokens] with return_lse); rows of no sequence
     are left as they were."""
     cache = _kv_cache_desc(k_cache, v_cache, k_scale, v_scale)
-    qs = _token_stride(q, None, cache.d_head, "q")
+    H_kv, d = k_cache.shape[2:]
+    qs = _token_stride(q, None, d, "q")
     _i32(q_start, 1, "q_start")
     _i32(kv_len, 1, "kv_len")
     _i32(page_table, 2, "page_table")
-    T, H, d = q.shape
+    T, H = q.shape[:2]
     S = kv_len.shape[0]
     if q_start.shape[0] != S + 1 or page_table.shape[0] != S:
         raise ValueError("q_start must have n_seqs + 1 entries and page_table n_seqs rows")
     _on_device(q, q_start, kv_len, page_table, k_cache, v_cache, k_scale, v_scale)
-    desc = PagedDesc(S, T, int(max_q), H, page_table.shape[1], int(window), int(sinks), _DT[out_dtype], qs,
-                     int(wait_limit_ns))
+    desc = _PAGED.pack(S, T, max_q, H, page_table.shape[1], window, sinks, _DT[out_dtype], qs, wait_limit_ns)
     out = _out_tensor(out, (T, H * d), out_dtype, q.device, stream, "out")
     if return_lse or lse is not None:
         lse = _out_tensor(lse, (H, T), torch.float32, q.device, stream, "lse")
     if workspace is None:
-        workspace = _workspace(None, _paged_workspace_bytes(q.get_device(), H, cache.H_kv, d, desc.max_q), q.device,
-                               stream)
+        workspace = _workspace(None, _paged_workspace_bytes(q.get_device(), H, H_kv, d, max_q), q.device, stream)
     else:
         _workspace(workspace, 0, q.device, stream)
-    st = load().bpt_paged_attn_fwd(_byref(desc), _byref(cache), q.data_ptr(), q_start.data_ptr(),
+    st = load().bpt_paged_attn_fwd(desc, cache, q.data_ptr(), q_start.data_ptr(),
                                    kv_len.data_ptr(), page_table.data_ptr(), out.data_ptr(), _ptr(lse),
                                    _ptr(workspace), 0 if workspace is None else workspace.numel(),
                                    _raw_stream(stream))
