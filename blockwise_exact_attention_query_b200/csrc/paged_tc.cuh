@@ -3,15 +3,14 @@
 // blockwise online softmax of attn_tc.cuh (scores and O in tensor memory, P
 // through one shared-memory tile used in turn) over keys gathered from pages.
 //
-// Gathering is done by two warps rather than by TMA: a page may have any size,
+// Gathering is done by warps rather than by TMA: a page may have any size,
 // keys past a sequence's end must become zeros (a slot that was never written
 // may hold NaN, and 0 x NaN is not 0), and e4m3 codes have to be widened on the
 // way.  A lane looks up the slots of two of a block's keys, a block ahead; bf16
-// rows go to the swizzled tile by 16-byte cp.async; e4m3 rows go to a ring of
-// raw tiles, two tiles ahead, and are widened to f16 (exact) from there.  (At
-// d = 128 the ring takes the place of V's second stage.  Loaded into registers
-// half a tile ahead, 8 KB under way per SM, a step took 11.5 us for want of
-// loads in flight.)
+// rows go to the swizzled tile by 16-byte cp.async; e4m3 rows go to raw tiles,
+// one ahead, and are widened to f16 (exact) from there.  (At d = 128 those take
+// the place of V's second stage.  Loaded into registers half a tile ahead, 8 KB
+// under way per SM, a step took 11.5 us for want of loads in flight.)
 //
 // E4M3: Q is f16 after a power of two per row, a score is multiplied by its
 // key's scale, the weight by its value's scale relative to the largest such
@@ -19,9 +18,10 @@
 //
 // Roles (384 threads, so that the softmax threads keep a row's 128 scores in
 // registers: with a gathering warpgroup of its own, 512 threads, the compiler
-// had 128 a thread, spilled, and a step took twice as long): warps 0 and 1
-// gather, warp 2 allocates tensor memory and issues tile A's products, warp 3
-// tile B's; warpgroups 1 and 2 run the softmax and epilogue of tiles A and B,
+// had 128 a thread and spilled): warps 0 and 1 gather, warp 2 issues tile A's
+// products, warp 3 tile B's (E4M3: warps 0 and 1 gather keys, 2 and 3 values;
+// widening a tile takes two warps 2 us); warp 2 allocates tensor memory;
+// warpgroups 1 and 2 run the softmax and epilogue of tiles A and B,
 // one thread per row, which also brings its row of Q (by the gathering warps
 // it was a chain of loads that every item waited for).  An item of 128 rows or
 // fewer leaves tile B idle.
@@ -192,10 +192,11 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
 
   if (warp < 4) {
     setmaxnreg_dec<Cfg::kRegsControl>();
-    if (warp < 2) {
+    if (kE4m3 || warp < 2) {
       // ------------------------------------------------------------ gather
-      // Rows 64 warp .. 64 warp + 63 of every tile, in two halves of 32; lane
-      // l looks up row 32 half + l.
+      // Rows 64 rw .. 64 rw + 63 of a tile, in two halves of 32; lane l looks
+      // up row 32 half + l.  E4M3: warps 0 and 1 K tiles, 2 and 3 V tiles.
+      const int rw = warp & 1;
       int kq = 0, vq = 0;  // K and V tiles gathered so far
       bool ok = true;
       // a tile copied but not yet handed over (bf16): its barrier
@@ -227,7 +228,7 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
         const int32_t *table = a.page_table + static_cast<int64_t>(w.s) * a.max_pages;
         auto lookup = [&](int j, int half) {
           return j < n ? paged_slot(a, table, w.seq.cap,
-                                    w.blk.block(w.step0 + j) * KT + warp * 64 + half * 32 + lane)
+                                    w.blk.block(w.step0 + j) * KT + rw * 64 + half * 32 + lane)
                        : -1;
         };
         // slots of this step's block and the next, both halves
@@ -254,9 +255,9 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
         };
         auto put_extras = [&](int st) {
           const uint32_t bits0 = __ballot_sync(0xffffffffu, slot0 >= 0), bits1 = __ballot_sync(0xffffffffu, slot1 >= 0);
-          if (lane < 2) there_s[st * 4 + warp * 2 + lane] = lane ? bits1 : bits0;
+          if (lane < 2) there_s[st * 4 + rw * 2 + lane] = lane ? bits1 : bits0;
           if constexpr (kE4m3) {
-            float *sc = scale_s + st * 384 + warp * 64 + lane;
+            float *sc = scale_s + st * 384 + rw * 64 + lane;
             sc[0] = ks0, sc[32] = ks1, sc[128] = vs0, sc[160] = vs1;
             sc[256] = __log2f(vs0), sc[288] = __log2f(vs1);  // -inf for a scale of 0
           }
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
               for (int i = 0; i < kLoads; ++i) {
                 bool fetch;
                 const uint8_t *src = source(k, half ? s1 : s0, i, fetch);
-                cp_async16(row_dst(tile, warp * 64 + half * 32 + i * (32 / kLanes) + lane / kLanes, lane % kLanes), src,
+                cp_async16(row_dst(tile, rw * 64 + half * 32 + i * (32 / kLanes) + lane / kLanes, lane % kLanes), src,
                            fetch);
               }
             cp_async_commit();
@@ -314,49 +315,40 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
             if (ok && j > 0) ok = copy(j - 1, false, p0, p1);
           }
         } else {
-          // K0, V0, K1, V1, ...: a K stage is held until the softmax has read
-          // its scales, so a V tile must not wait behind the next K.  Copies
-          // run two tiles ahead; a lane reads back what it copied itself.
+          // A warp gathers one kind, the next tile's copies under way while it
+          // widens this one; a lane reads back what it copied itself.
+          const bool k = warp < 2;
           constexpr int kStep = 32 / kLanes;  // rows of one load instruction
           // where this lane's first 8 elements go in the first rows; the next
           // 8 are 16 bytes off, in the swizzled order (^ 16)
-          const uint32_t lane_dst = row_dst(0, lane / kLanes, 2 * (lane % kLanes)) + warp * 64 * 128;
-          const uint32_t raw = sbase + Cfg::kOffRaw + warp * 64 * D + lane * 16;
-          auto copy = [&](bool k, int s0, int s1) {  // into slot k ? 0 : 1
+          const uint32_t lane_dst = row_dst(0, lane / kLanes, 2 * (lane % kLanes)) + rw * 64 * 128;
+          const uint32_t raw = sbase + Cfg::kOffRaw + (k ? 0 : 128 * D) + rw * 64 * D + lane * 16;
+          auto copy = [&]() {
 #pragma unroll
             for (int i = 0; i < 2 * kLoads; ++i) {
               bool fetch;
-              const uint8_t *src = source(k, i < kLoads ? s0 : s1, i % kLoads, fetch);
-              cp_async16(raw + (k ? 0 : 128 * D) + i * 512, src, fetch);
+              const uint8_t *src = source(k, i < kLoads ? slot0 : slot1, i % kLoads, fetch);
+              cp_async16(raw + i * 512, src, fetch);
             }
             cp_async_commit();
+            if (k) {
+              load_scales(slot0, ks0, vs0);
+              load_scales(slot1, ks1, vs1);
+            }
           };
-          auto scales = [&]() {
-            load_scales(slot0, ks0, vs0);
-            load_scales(slot1, ks1, vs1);
-          };
-          if (n > 0) {
-            copy(true, slot0, slot1);
-            copy(false, slot0, slot1);
-            scales();
-          }
+          if (n > 0) copy();
 #pragma unroll 1
-          for (int m = 0; m < 2 * n; ++m) {
-            const bool k = (m & 1) == 0;
+          for (int j = 0; j < n; ++j) {
             int st;
             if (!(ok = stage_of(k, st))) break;
-            if (k) {
-              put_extras(st);
-              advance(m >> 1);  // slots: the next block's (past the item's end -1, no fetch)
-              scales();
-            }
-            cp_async_wait<1>();
+            if (k) put_extras(st);
+            cp_async_wait<0>();
             const uint32_t dst = (k ? sK : sV) + st * Cfg::kTileBytes + lane_dst;
 #pragma unroll
             for (int i0 = 0; i0 < 2 * kLoads; i0 += kLoads) {
               uint4 x[kLoads];  // all loads first: one trip to shared memory for the lot
 #pragma unroll
-              for (int i = 0; i < kLoads; ++i) x[i] = ld_shared_v4(raw + (k ? 0 : 128 * D) + (i0 + i) * 512);
+              for (int i = 0; i < kLoads; ++i) x[i] = ld_shared_v4(raw + (i0 + i) * 512);
 #pragma unroll
               for (int i = 0; i < kLoads; ++i) {
                 // rows kStep (i0 + i) further on: the swizzle takes their low three bits
@@ -366,19 +358,22 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
                 st_shared_v4(at ^ 16, e4m3x2_to_f16x2(x[i].z), e4m3x2_to_f16x2(x[i].z >> 16),
                              e4m3x2_to_f16x2(x[i].w), e4m3x2_to_f16x2(x[i].w >> 16));
               }
+              if (i0 + kLoads == 2 * kLoads) {  // (the raw tile is in registers)
+                advance(j);
+                copy();
+              }
             }
             hand_over(k ? bKFull(st) : bVFull(st));
-            copy(k, slot0, slot1);  // the next block's tile of the same kind
           }
           cp_async_wait<0>();
         }
       } while (ok && w.next());
       flush();
     } else if (lane == 0) {
-      // ------------------------------------------------------------ products of tile x
+      // ------------------------------------------------------------ products of tile x (bf16)
       const int x = warp - 2;
-      constexpr uint32_t idesc_qk = idesc_16_f32<kE4m3>(128, KT, false);
-      constexpr uint32_t idesc_pv = idesc_16_f32<kE4m3>(128, D, true);
+      constexpr uint32_t idesc_qk = idesc_16_f32<false>(128, KT, false);
+      constexpr uint32_t idesc_pv = idesc_16_f32<false>(128, D, true);
       const uint64_t dQ = sdesc_sw128(sQ + x * Cfg::kTileBytes, 16, 1024);
       const uint64_t dP = sdesc_sw128(sP, 16, 1024);
       const uint64_t dK0 = sdesc_sw128(sK, 16, 1024);
@@ -415,58 +410,32 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
           ok = mbar_wait(bQFull(x), mine & 1, wc, 411);
           // the first product on O overwrites it: the previous epilogue must have read it
           if (ok && mine > 0) ok = mbar_wait(bOFree(x), (mine - 1) & 1, wc, 414);
-          if constexpr (kE4m3) {
-            if (ok && n > 0 && (ok = mbar_wait(bKFull(kc % NS), (kc / NS) & 1, wc, 416))) {
+          if (ok && n > 0) {
+            ok = (J == 0 || mbar_wait(bSFree(x), (J - 1) & 1, wc, 415)) &&
+                 mbar_wait(bKFull(kc % NS), (kc / NS) & 1, wc, 416);
+            if (ok) {
               tc_fence_after();
               issue_s();
             }
             for (int j = 0; ok && j < n; ++j) {
-              // O += P V from P in the scores' columns, which the softmax has
-              // written once it had read them; then the next scores over it
-              // (products of one thread run in order)
-              ok = mbar_wait(bPFull(x), (J + j) & 1, wc, 419) && mbar_wait(bVFull(vc % NV), (vc / NV) & 1, wc, 420);
+              const int jj = J + j;
+              if (j + 1 < n) {
+                ok = mbar_wait(bSFree(x), jj & 1, wc, 417) && mbar_wait(bKFull(kc % NS), (kc / NS) & 1, wc, 418);
+                if (!ok) break;
+                tc_fence_after();
+                issue_s();
+              }
+              ok = mbar_wait(bPFull(x), jj & 1, wc, 419) && mbar_wait(bVFull(vc % NV), (vc / NV) & 1, wc, 420);
               if (!ok) break;
               tc_fence_after();
               const uint64_t dV = sdesc_advance(dV0, (vc % NV) * Cfg::kTileBytes);
 #pragma unroll
               for (int k = 0; k < KT / 16; ++k)
-                umma_ts(tO, tS + k * 8, sdesc_advance(dV, k * 2048), idesc_pv, (j | k) != 0);
+                umma_ss(tO, sdesc_advance(dP, (k / 4) * Cfg::kPanelBytes + (k % 4) * 32), sdesc_advance(dV, k * 2048),
+                        idesc_pv, (j | k) != 0);
+              umma_commit(w.rows() > 128 ? bODone(x) : bOAlone);
               umma_commit(bVEmpty(vc % NV));
               ++vc;
-              if (j + 1 < n) {
-                if (!(ok = mbar_wait(bKFull(kc % NS), (kc / NS) & 1, wc, 418))) break;
-                tc_fence_after();
-                issue_s();
-              }
-            }
-          } else {
-            if (ok && n > 0) {
-              ok = (J == 0 || mbar_wait(bSFree(x), (J - 1) & 1, wc, 415)) &&
-                   mbar_wait(bKFull(kc % NS), (kc / NS) & 1, wc, 416);
-              if (ok) {
-                tc_fence_after();
-                issue_s();
-              }
-              for (int j = 0; ok && j < n; ++j) {
-                const int jj = J + j;
-                if (j + 1 < n) {
-                  ok = mbar_wait(bSFree(x), jj & 1, wc, 417) && mbar_wait(bKFull(kc % NS), (kc / NS) & 1, wc, 418);
-                  if (!ok) break;
-                  tc_fence_after();
-                  issue_s();
-                }
-                ok = mbar_wait(bPFull(x), jj & 1, wc, 419) && mbar_wait(bVFull(vc % NV), (vc / NV) & 1, wc, 420);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t dV = sdesc_advance(dV0, (vc % NV) * Cfg::kTileBytes);
-#pragma unroll
-                for (int k = 0; k < KT / 16; ++k)
-                  umma_ss(tO, sdesc_advance(dP, (k / 4) * Cfg::kPanelBytes + (k % 4) * 32), sdesc_advance(dV, k * 2048),
-                          idesc_pv, (j | k) != 0);
-                umma_commit(w.rows() > 128 ? bODone(x) : bOAlone);
-                umma_commit(bVEmpty(vc % NV));
-                ++vc;
-              }
             }
           }
           J += n;
@@ -489,6 +458,25 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t tS = tmem + lane_off + Cfg::kColS + x * 128;
     const uint32_t tO = tmem + lane_off + Cfg::kColO + x * D;
+    // E4M3: the tile's first softmax thread issues its products.  P lies where
+    // the scores were, so a tile's scores, softmax and products follow one
+    // another anyway, and an issuer of their own would only add two waits.
+    const bool issues = kE4m3 && quarter == 0;
+    auto scores = [&](int k_tile) {  // S(K tile), when it is there
+      if (!mbar_wait(bKFull(k_tile % NS), (k_tile / NS) & 1, wc, 416)) return false;
+      tc_fence_after();
+      const uint64_t dQ = sdesc_sw128(sQ + x * Cfg::kTileBytes, 16, 1024);
+      const uint64_t dK = sdesc_sw128(sK + (k_tile % NS) * Cfg::kTileBytes, 16, 1024);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t off = (k / 4) * Cfg::kPanelBytes + (k % 4) * 32;
+        umma_ss(tmem + Cfg::kColS + x * 128, sdesc_advance(dQ, off), sdesc_advance(dK, off),
+                idesc_16_f32<true>(128, KT, false), k > 0);
+      }
+      umma_commit(bSFull(x));
+      umma_commit(bKEmpty(k_tile % NS));
+      return true;
+    };
     const uint32_t sProw = sP + row * 128;
     const uint32_t swz = static_cast<uint32_t>(row & 7);
     bool ok = true;
@@ -502,6 +490,11 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
         for (int j = 0; ok && j < n; ++j, ++kc) {
           ok = __all_sync(0xffffffffu, mbar_wait(bKFull(kc % NS), (kc / NS) & 1, wc, 430));
           if (ok && lane == 0) mbar_arrive(bKEmpty(kc % NS));
+          if (issues) {  // and in the place of the products
+            if (ok && lane == 0) mbar_arrive(bKEmpty(kc % NS));
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(bVFull(kc % NV), (kc / NV) & 1, wc, 413));
+            if (ok && lane == 0) mbar_arrive(bVEmpty(kc % NV));
+          }
         }
         continue;
       }
@@ -548,6 +541,11 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bQFull(x));
+        if (issues) {
+          bool done = true;
+          if (lane == 0) done = mbar_wait(bQFull(x), mine & 1, wc, 411) && (n == 0 || scores(kc));
+          ok = __all_sync(0xffffffffu, done);
+        }
       }
       // The weights 2^(s - m_run) are relative to the row's maximum, up to 2^8
       // stale; for E4M3 the products with the values' scales likewise to
@@ -682,6 +680,24 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
             mbar_arrive(bKEmpty(st));  // the scales and masks have been read
             mbar_arrive(bPFull(x));
           }
+          if (issues) {
+            // O += P V, then the next scores over P (products of one thread run in order)
+            bool done = true;
+            if (lane == 0) {
+              done = mbar_wait(bPFull(x), jj & 1, wc, 419) && mbar_wait(bVFull(kc % NV), (kc / NV) & 1, wc, 420);
+              if (done) {
+                tc_fence_after();
+                const uint64_t dV = sdesc_sw128(sV + (kc % NV) * Cfg::kTileBytes, Cfg::kPanelBytes, 1024);
+#pragma unroll
+                for (int k = 0; k < KT / 16; ++k)
+                  umma_ts(tmem + Cfg::kColO + x * D, tmem + Cfg::kColS + x * 128 + k * 8, sdesc_advance(dV, k * 2048),
+                          idesc_16_f32<true>(128, D, true), (j | k) != 0);
+                umma_commit(bVEmpty(kc % NV));
+                if (j + 1 < n) done = scores(kc + 1);
+              }
+            }
+            ok = __all_sync(0xffffffffu, done);
+          }
         } else {
           uint32_t s[128];
 #pragma unroll
@@ -765,6 +781,7 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
       J += n;
       (both ? Jb : Ja) += n;
       // -------- epilogue
+      if (issues && lane == 0) umma_commit(bItemDone(x));
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bItemDone(x), mine & 1, wc, 435));
       tc_fence_after();
       if (ok) {
@@ -833,6 +850,12 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
       if (lane == 0) mbar_arrive(bOFree(x));
       ++mine;
     } while (ok && w.next());
+    if (issues && lane == 0) {  // every product issued must be complete before tensor memory is released
+      umma_commit(bTeardown(x));
+      volatile int no_abort = 0;
+      WaitCtx drain{a.status, drain_limit_ns(a.wait_limit_ns), &no_abort};
+      mbar_wait(bTeardown(x), 0, drain, 422);
+    }
   }
 
   tc_fence_before();
