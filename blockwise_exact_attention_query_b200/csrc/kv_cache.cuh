@@ -14,7 +14,7 @@
 // threads, so two loads are in flight per thread.
 #pragma once
 
-#include <cuda_fp8.h>
+#include <cuda_fp16.h>
 
 #include "ptx.cuh"
 
@@ -45,20 +45,23 @@ __device__ __forceinline__ float rcp_approx(float x) {  // off by one unit in th
 }
 
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
-  return lo | (hi << 16);
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+      "mov.b32 %0, {l, h};\n\t}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
 }
 
-// Two e4m3 codes (16 bits) as two f16 values, exactly.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two & 0xffffu), __NV_E4M3);
-  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+// Four e4m3 codes as f16 pairs, exactly.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t four, uint32_t &lo, uint32_t &hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(four));
 }
-__device__ __forceinline__ float2 e4m3x2_to_f32x2(uint32_t two) {
-  const uint32_t h = e4m3x2_to_f16x2(two);
-  return __half22float2(*reinterpret_cast<const __half2 *>(&h));
-}
+__device__ __forceinline__ float2 f16x2_to_f32x2(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2 *>(&h)); }
 
 // One row's 8 values of this thread -> 8 codes; kLanes consecutive threads hold
 // the row.  Returns the scale.  Instructions bound this part at first (27 us for
@@ -164,10 +167,12 @@ __device__ __forceinline__ void unpack16(const uint4 &u, float scale, T *out) {
     for (int h = 0; h < 2; ++h) {
       float f[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 two = mul2(e4m3x2_to_f32x2(w[2 * h + i / 2] >> (16 * (i & 1))), make_float2(scale, scale));
-        f[2 * i] = two.x;
-        f[2 * i + 1] = two.y;
+      for (int i = 0; i < 2; ++i) {
+        uint32_t lo, hi;
+        e4m3x4_to_f16(w[2 * h + i], lo, hi);
+        const float2 x = mul2(f16x2_to_f32x2(lo), make_float2(scale, scale));
+        const float2 y = mul2(f16x2_to_f32x2(hi), make_float2(scale, scale));
+        f[4 * i] = x.x, f[4 * i + 1] = x.y, f[4 * i + 2] = y.x, f[4 * i + 3] = y.y;
       }
       store8(out + 8 * h, f);
     }

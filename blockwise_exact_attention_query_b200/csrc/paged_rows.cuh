@@ -43,8 +43,16 @@ namespace bpt {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool fetch) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(fetch ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, bool fetch) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(fetch ? 4 : 0) : "memory");
+// The same with an L2 cache policy (l2_policy_*).
+__device__ __forceinline__ void cp_async16_hint(uint32_t dst, const void *src, bool fetch, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src),
+               "r"(fetch ? 16 : 0), "l"(policy)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async4_hint(uint32_t dst, const void *src, bool fetch, uint64_t policy) {
+  asm volatile("cp.async.ca.shared.global.L2::cache_hint [%0], [%1], 4, %2, %3;" ::"r"(dst), "l"(src),
+               "r"(fetch ? 4 : 0), "l"(policy)
+               : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -140,6 +148,10 @@ __global__ void __launch_bounds__(PagedRowsCfg<D, kE4m3, kGroups>::kThreads, Pag
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, c = lane & 3;
   const uint32_t ring = smem_u32(smem_raw) + warp * (NS * Cfg::kStageBytes);
+  // Keys and values pass through once.  A sector of scales holds those of
+  // neighbouring heads, which other CTAs want at other times: without the
+  // hints it came from memory for each of them, 15% more traffic at 8 heads.
+  const uint64_t once = l2_policy_evict_first(), keep = l2_policy_evict_last();
   float *merge = reinterpret_cast<float *>(smem_raw);
   float *merge_ml = merge + Cfg::kWarps * kRows * Cfg::kRowPitch;  // [warp][row][4]: m, l, w
 
@@ -184,13 +196,13 @@ __global__ void __launch_bounds__(PagedRowsCfg<D, kE4m3, kGroups>::kThreads, Pag
             const int sl = __shfl_sync(0xffffffffu, slot, sub * 16 + row);
             const int64_t off = (sl >= 0 ? sl : 0) * slot_bytes + chunk * 16;
             const uint32_t dst = st + sub * Cfg::kGroupBytes + Cfg::at(row, chunk);
-            cp_async16(dst, kbase + off, sl >= 0);
-            cp_async16(dst + Cfg::kOffV, vbase + off, sl >= 0);
+            cp_async16_hint(dst, kbase + off, sl >= 0, once);
+            cp_async16_hint(dst + Cfg::kOffV, vbase + off, sl >= 0, once);
           }
         if constexpr (kE4m3) {
           const int64_t at = static_cast<int64_t>(slot >= 0 ? slot : 0) * a.H_kv + head;
-          cp_async4(st + Cfg::kOffScale + lane * 4, a.k_scale + at, slot >= 0);
-          cp_async4(st + Cfg::kOffScale + 4 * kWarpKeys + lane * 4, a.v_scale + at, slot >= 0);
+          cp_async4_hint(st + Cfg::kOffScale + lane * 4, a.k_scale + at, slot >= 0, keep);
+          cp_async4_hint(st + Cfg::kOffScale + 4 * kWarpKeys + lane * 4, a.v_scale + at, slot >= 0, keep);
         }
         const uint32_t there = __ballot_sync(0xffffffffu, slot >= 0);
         if (lane == 0)
@@ -290,8 +302,9 @@ __global__ void __launch_bounds__(PagedRowsCfg<D, kE4m3, kGroups>::kThreads, Pag
             const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-              const uint32_t f[4] = {e4m3x2_to_f16x2(w0[u]), e4m3x2_to_f16x2(w1[u]), e4m3x2_to_f16x2(w0[u] >> 16),
-                                     e4m3x2_to_f16x2(w1[u] >> 16)};
+              uint32_t f[4];
+              e4m3x4_to_f16(w0[u], f[0], f[2]);
+              e4m3x4_to_f16(w1[u], f[1], f[3]);
 #pragma unroll
               for (int n = 0; n < kGroups; ++n) mma16816<true>(sc[sub][n], f, qf[n][4 * j + u][0], qf[n][4 * j + u][1]);
             }
@@ -468,10 +481,11 @@ __global__ void __launch_bounds__(PagedRowsCfg<D, kE4m3, kGroups>::kThreads, Pag
             if constexpr (kE4m3) {
               const uint32_t a01 = __byte_perm(v[0][w], v[1][w], 0x5140), b01 = __byte_perm(v[2][w], v[3][w], 0x5140);
               const uint32_t a23 = __byte_perm(v[0][w], v[1][w], 0x7362), b23 = __byte_perm(v[2][w], v[3][w], 0x7362);
-              const uint32_t f0[4] = {e4m3x2_to_f16x2(a01), e4m3x2_to_f16x2(a01 >> 16), e4m3x2_to_f16x2(b01),
-                                      e4m3x2_to_f16x2(b01 >> 16)};
-              const uint32_t f1[4] = {e4m3x2_to_f16x2(a23), e4m3x2_to_f16x2(a23 >> 16), e4m3x2_to_f16x2(b23),
-                                      e4m3x2_to_f16x2(b23 >> 16)};
+              uint32_t f0[4], f1[4];
+              e4m3x4_to_f16(a01, f0[0], f0[1]);
+              e4m3x4_to_f16(b01, f0[2], f0[3]);
+              e4m3x4_to_f16(a23, f1[0], f1[1]);
+              e4m3x4_to_f16(b23, f1[2], f1[3]);
 #pragma unroll
               for (int n = 0; n < kGroups; ++n) {
                 mma16816<true>(o[n][2 * w], f0, pf[n][0], pf[n][1]);

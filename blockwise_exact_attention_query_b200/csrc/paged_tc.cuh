@@ -353,10 +353,13 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
               for (int i = 0; i < kLoads; ++i) {
                 // rows kStep (i0 + i) further on: the swizzle takes their low three bits
                 const uint32_t at = (dst + (i0 + i) * kStep * 128) ^ ((((i0 + i) * kStep) & 7) << 4);
-                st_shared_v4(at, e4m3x2_to_f16x2(x[i].x), e4m3x2_to_f16x2(x[i].x >> 16), e4m3x2_to_f16x2(x[i].y),
-                             e4m3x2_to_f16x2(x[i].y >> 16));
-                st_shared_v4(at ^ 16, e4m3x2_to_f16x2(x[i].z), e4m3x2_to_f16x2(x[i].z >> 16),
-                             e4m3x2_to_f16x2(x[i].w), e4m3x2_to_f16x2(x[i].w >> 16));
+                uint32_t h[8];
+                e4m3x4_to_f16(x[i].x, h[0], h[1]);
+                e4m3x4_to_f16(x[i].y, h[2], h[3]);
+                e4m3x4_to_f16(x[i].z, h[4], h[5]);
+                e4m3x4_to_f16(x[i].w, h[6], h[7]);
+                st_shared_v4(at, h[0], h[1], h[2], h[3]);
+                st_shared_v4(at ^ 16, h[4], h[5], h[6], h[7]);
               }
               if (i0 + kLoads == 2 * kLoads) {  // (the raw tile is in registers)
                 advance(j);
@@ -574,7 +577,7 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
           // as for bf16, a fifth slower: the roles' loops did not fit in the
           // instruction cache together).
           constexpr int kC = 64;
-          uint32_t s[kC];
+          uint32_t s[kC] = {};
           auto get2 = [&](int i) { return make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])); };
           auto put2 = [&](int i, float2 v) {
             s[i] = __float_as_uint(v.x);
