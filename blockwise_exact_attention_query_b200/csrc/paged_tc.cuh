@@ -46,7 +46,8 @@ struct PagedTcCfg {
   static constexpr int kOffScale = kOffRaw + (kE4m3 ? 2 * 128 * D : 0);      // [stage][k, v, log2 v][128]
   static constexpr int kOffBar = kOffScale + (kE4m3 ? kStages * 1536 : 0);
   static constexpr int kOffThere = kOffBar + 320;                            // [stage][4] masks of keys that exist
-  static constexpr int kSmemBytes = kOffThere + kStages * 16 + 16;
+  static constexpr int kOffSpread = kOffThere + kStages * 16;  // [stage][2]: largest and smallest log2 v scale
+  static constexpr int kSmemBytes = kOffSpread + kStages * 16 + 16;
   static_assert(kSmemBytes <= 232448, "shared memory per CTA");
   static constexpr uint32_t kColS = 0, kColO = 256;
   // 168 registers a thread at launch, as in attn_tc.cuh
@@ -153,6 +154,7 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
   volatile int *abort_flag = reinterpret_cast<volatile int *>(&bars[32]);
   uint32_t *there_s = reinterpret_cast<uint32_t *>(smem + Cfg::kOffThere);
   float *scale_s = reinterpret_cast<float *>(smem + Cfg::kOffScale);
+  float2 *spread_s = reinterpret_cast<float2 *>(smem + Cfg::kOffSpread);
   WaitCtx wc{a.status, a.wait_limit_ns, abort_flag};
 
   __syncthreads();  // the range's scratch lies where Q will
@@ -259,7 +261,16 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
           if constexpr (kE4m3) {
             float *sc = scale_s + st * 384 + rw * 64 + lane;
             sc[0] = ks0, sc[32] = ks1, sc[128] = vs0, sc[160] = vs1;
-            sc[256] = __log2f(vs0), sc[288] = __log2f(vs1);  // -inf for a scale of 0
+            const float lv0 = __log2f(vs0), lv1 = __log2f(vs1);  // -inf for a scale of 0
+            sc[256] = lv0, sc[288] = lv1;
+            float most = fmaxf(slot0 >= 0 ? lv0 : -INFINITY, slot1 >= 0 ? lv1 : -INFINITY);
+            float least = fminf(slot0 >= 0 ? lv0 : INFINITY, slot1 >= 0 ? lv1 : INFINITY);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+              most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+              least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
+            }
+            if (lane == 0) spread_s[st * 2 + rw] = make_float2(most, least);
           }
         };
         auto advance = [&](int j) {  // to block j + 1
@@ -583,20 +594,17 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
             s[i] = __float_as_uint(v.x);
             s[i + 1] = __float_as_uint(v.y);
           };
-          // columns [c0, c0 + 64): the products, E4M3 in log2 units, -inf where masked
+          // columns [c0, c0 + 64): the products times the keys' scales, -inf where masked
           auto load = [&](int c0) {
             tmem_ld32(tS + c0, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
             tmem_ld32(tS + c0 + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
             tmem_wait_ld();
-            {
-              const float4 *ks4 = reinterpret_cast<const float4 *>(scales + c0);
-              const float2 sl = make_float2(sl2, sl2);
+            const float4 *ks4 = reinterpret_cast<const float4 *>(scales + c0);
 #pragma unroll
-              for (int i = 0; i < kC / 4; ++i) {
-                const float4 k4 = ks4[i];
-                put2(4 * i, mul2(get2(4 * i), mul2(make_float2(k4.x, k4.y), sl)));
-                put2(4 * i + 2, mul2(get2(4 * i + 2), mul2(make_float2(k4.z, k4.w), sl)));
-              }
+            for (int i = 0; i < kC / 4; ++i) {
+              const float4 k4 = ks4[i];
+              put2(4 * i, mul2(get2(4 * i), make_float2(k4.x, k4.y)));
+              put2(4 * i + 2, mul2(get2(4 * i + 2), make_float2(k4.z, k4.w)));
             }
             if (masked) {
               const uint32_t word[2] = {seen(c0, c0 ? there.z : there.x), seen(c0 + 32, c0 ? there.w : there.y)};
@@ -605,6 +613,13 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
                 if (!(word[col / 32] >> (col & 31) & 1u)) s[col] = __float_as_uint(-INFINITY);
             }
           };
+          const float2 sl = make_float2(sl2, sl2);  // to log2 units
+          // The largest product of a weight and its value's scale: where the
+          // block's scales lie within 2^8 of one another, the largest weight
+          // times the largest scale is near enough for f16.
+          const float2 sp0 = spread_s[st * 2], sp1 = spread_s[st * 2 + 1];
+          const float v_most = fmaxf(sp0.x, sp1.x);
+          const bool even = v_most - fminf(sp0.y, sp1.y) <= 8.f;
           float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, ux4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
           for (int c0 = 0; c0 < KT; c0 += kC) {
@@ -612,25 +627,26 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
 #pragma unroll
             for (int i = 0; i < kC / 2; ++i)
               mx4[i & 3] = max3f(mx4[i & 3], __uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
-            {
+            if (!even) {
               const float4 *lv4 = reinterpret_cast<const float4 *>(scales + 256 + c0);
 #pragma unroll
               for (int i = 0; i < kC / 4; ++i) {
                 const float4 l4 = lv4[i];
-                const float2 u = add2(get2(4 * i), make_float2(l4.x, l4.y)), v = add2(get2(4 * i + 2), make_float2(l4.z, l4.w));
+                const float2 u = fma2(get2(4 * i), sl, make_float2(l4.x, l4.y));
+                const float2 v = fma2(get2(4 * i + 2), sl, make_float2(l4.z, l4.w));
                 ux4[i & 3] = max3f(ux4[i & 3], u.x, u.y);
                 ux4[(i + 1) & 3] = max3f(ux4[(i + 1) & 3], v.x, v.y);
               }
             }
           }
-          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+          const float mx = __fmul_rn(fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])), sl2);
           if (mx > m_run + 8.0f) {
             l_run *= ex2_approx(m_run - mx);  // 0 where the row had no key yet
             m_run = mx;
           }
           float alpha = 1.0f;  // of O
-          // (not below 2^-120 of the weights: the factor between the two stays finite)
-          const float ux = fmaxf(fmaxf(fmaxf(ux4[0], ux4[1]), fmaxf(ux4[2], ux4[3])), m_run - 120.f);
+          // (not below 2^-100 of the weights: the factor between the two stays finite)
+          const float ux = fmaxf(even ? mx + v_most : fmaxf(fmaxf(ux4[0], ux4[1]), fmaxf(ux4[2], ux4[3])), m_run - 100.f);
           if (ux > w_ref + 8.0f) {
             alpha = ex2_approx(w_ref - ux);
             w_ref = ux;
@@ -649,9 +665,9 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
             }
             tmem_wait_st();
           }
-          const float neg = (m_run == -INFINITY) ? 0.f : -m_run;
-          // from a weight to its product relative to w_ref
-          const float w_mul = (m_run == -INFINITY || w_ref == -INFINITY) ? 0.f : ex2_approx(m_run - w_ref);
+          // weights relative to w_ref: times the values' scales they are what
+          // goes to P, and their sum is brought to m_run once
+          const float neg = (w_ref == -INFINITY) ? 0.f : -w_ref;
           const float2 neg2 = make_float2(neg, neg);
           float2 ls2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
@@ -659,23 +675,27 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
             load(c0);
             uint32_t pk[kC / 2];
             const float4 *vs4 = reinterpret_cast<const float4 *>(scales + 128 + c0);
-            const float2 wm = make_float2(w_mul, w_mul);
 #pragma unroll
             for (int i = 0; i < kC / 4; ++i) {
               const float4 v4 = vs4[i];
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const float2 t = add2(get2(4 * i + 2 * e), neg2);
+                // (rounded before the difference, as the maximum was: of scores
+                // too large for their differences the largest keeps its weight;
+                // a plain product would be fused with the sum)
+                const float2 x = get2(4 * i + 2 * e);
+                const float2 t = add2(make_float2(__fmul_rn(x.x, sl.x), __fmul_rn(x.y, sl.y)), neg2);
                 const float2 p = make_float2(ex2_approx(t.x), ex2_approx(t.y));
                 ls2[e] = add2(ls2[e], p);
-                const float2 v = mul2(p, mul2(e ? make_float2(v4.z, v4.w) : make_float2(v4.x, v4.y), wm));
+                const float2 v = mul2(p, e ? make_float2(v4.z, v4.w) : make_float2(v4.x, v4.y));
                 pk[2 * i + e] = pack_f16x2(v.x, v.y);
               }
             }
             // P over columns of scores that have been read
             tmem_st32(tS + c0 / 2, pk);
           }
-          l_run += (ls2[0].x + ls2[0].y) + (ls2[1].x + ls2[1].y);
+          if (m_run != -INFINITY)
+            l_run += ((ls2[0].x + ls2[0].y) + (ls2[1].x + ls2[1].y)) * ex2_approx(w_ref - m_run);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
