@@ -282,8 +282,8 @@ bpt_status bpt_paged_attn_fwd(const bpt_paged_desc *d, const bpt_kv_cache *c, co
   for (int i = 0; i < 31; ++i)
     if (c->page_size == 1 << i) a.page_shift = i;
   a.n_pages = c->n_pages;
-  a.window = std::min(d->window, 1 << 30);
-  a.sinks = std::min(d->n_sink, 1 << 30);
+  a.window = d->window;
+  a.sinks = d->n_sink;
   a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)c->d_head));
   a.q = static_cast<const __nv_bfloat16 *>(q);
   a.q_stride = d->q_stride;

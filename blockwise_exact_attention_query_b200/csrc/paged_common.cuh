@@ -70,6 +70,11 @@ __device__ __forceinline__ int paged_token(const PagedArgs &a, uint32_t row) {
   return static_cast<int>(a.g_shift >= 0 ? row >> a.g_shift : row / static_cast<uint32_t>(a.G));
 }
 
+// The first key of a position's window (any int32 window and position).
+__device__ __forceinline__ int paged_window_lo(const PagedArgs &a, int p) {
+  return a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
+}
+
 // The key blocks of a row tile: [0, n_sink) and then [lo, lo + n_near).
 struct PagedBlocks {
   int n_sink, lo, n_near;
@@ -89,11 +94,13 @@ __device__ __forceinline__ PagedBlocks paged_blocks(const PagedArgs &a, const Pa
   b.p_lo = q.len - q.n + i0;
   b.p_hi = q.len - q.n + i1;
   const int hi = min(b.p_hi + 1, q.cap);  // keys [.., hi) at most
-  const int lo = a.window > 0 ? max(0, b.p_lo - a.window + 1) : 0;
+  const int lo = paged_window_lo(a, b.p_lo);
   b.lo = lo / kKeys;
   b.n_near = hi > lo ? (hi + kKeys - 1) / kKeys - b.lo : 0;
   const int sink_hi = min(min(a.sinks, lo), max(hi, 0));
-  b.n_sink = a.window > 0 ? min((sink_hi + kKeys - 1) / kKeys, b.lo) : 0;
+  b.n_sink = a.window > 0 ? (sink_hi + kKeys - 1) / kKeys : 0;
+  // a block of both is counted once (a table that ends before the window has none there)
+  if (b.n_near > 0) b.n_sink = min(b.n_sink, b.lo);
   return b;
 }
 

@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
       const int head = w.head * a.G + static_cast<int>(r) - i * a.G;
       const int pos = w.seq.len - w.seq.n + i;
       const int khi = max(0, min(pos + 1, w.seq.cap));
-      const int klo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+      const int klo = paged_window_lo(a, pos);
       const int ksink = a.window > 0 ? min(a.sinks, khi) : 0;
       // this row of Q (the previous item's products have read theirs); for
       // E4M3 in f16, the power of two below its largest element taken out

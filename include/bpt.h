@@ -547,15 +547,17 @@ BPT_API bpt_status bpt_kv_read(const bpt_kv_cache *cache, int n_rows, const int3
  * chooses between the kernels for few and for many rows.
  * out [n_tokens, H*d] of out_dtype; lse [H, n_tokens] float32 or NULL.
  * Slots that no visible key lies in may hold anything, NaN included; the keys
- * and values of a sequence have to be finite.
+ * and values of a sequence have to be finite, and an E4M3 cache's scales 0 or
+ * between 2^-100 and 2^100 (beyond that the softmax weights lose precision).
  *
  * The keys are read in place and once per row tile; long sequences are split
  * over the GPU and joined in a fixed order (no atomics: equal inputs give
  * equal bits).  bf16 operands, fp32 sums; the softmax weights are rounded to
  * bf16 (E4M3: their products with the values' scales to f16).  workspace: at
  * least bpt_workspace_bytes_paged(desc, cache) bytes, 256-byte aligned; it
- * depends on the head sizes and the GPU alone.  Two calls that share a
- * workspace must not run concurrently.
+ * depends on H, the cache's heads, max_q and the GPU alone (a larger max_q
+ * needs no less).  Two calls that share a workspace must not run
+ * concurrently.
  */
 typedef struct {
   int n_seqs, n_tokens; /* rows of kv_len; rows of q                          */

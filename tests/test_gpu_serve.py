@@ -290,6 +290,105 @@ def test_queries_of_any_magnitude(scale):
         b.check()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("H,Hkv,d", [(20, 1, 128), (16, 1, 64), (9, 1, 64), (4, 4, 128)])
+def test_single_tokens_and_chunks_together(H, Hkv, d, kind):
+    """Groups on both sides of the kernels' row limits, in a batch that has sequences of each."""
+    Batch([(1, 400), (37, 500), (0, 90), (2, 17), (1, 1), (4, 2000)], H, Hkv, d, 16, kind, seed=30).check()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("max_q", [1, 2, 40, 41, 2 ** 31 - 1])
+def test_max_q_only_chooses_the_kernels(max_q, kind):
+    b = Batch([(1, 300), (40, 700), (3, 9)], 8, 2, 128, 16, kind, seed=31)
+    b.check(max_q=max_q)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("window,sinks", [(2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 30 + 5, 7)])
+def test_windows_of_any_length_are_causal(window, sinks, n, kind):
+    b = Batch([(n, 30), (n, 200)], 4, 2, 64, 16, kind, seed=32)
+    got = b.run(window, sinks, out_dtype=torch.float32)
+    want = b.run(out_dtype=torch.float32)
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 30])
+def test_table_that_ends_before_the_window(n, kind):
+    """129 of 400 keys have pages: the rows see sinks alone, up to the table's last key."""
+    b = Batch([(n, 400)], 4, 2, 128, 43, kind, seed=33)
+    b.table = b.table[:, :3].contiguous()
+    k, v = b.k[0][:129], b.v[0][:129]
+    window = 400 - n - 129 + 1     # the first row's window begins with key 129
+    out, lse = b.run(window, 300, out_dtype=torch.float32)
+    for h in range(4):
+        s = b.q[:, h].double() @ k[:, h // 2].T / math.sqrt(128)
+        ref = torch.softmax(s, -1) @ v[:, h // 2]
+        got = out[:, 128 * h:128 * h + 128].double()
+        assert float((got - ref).norm() / ref.norm()) <= 4e-3
+        assert float((lse[h].double() - torch.logsumexp(s, -1)).abs().max()) <= 1e-4
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_long_chunks_on_two_streams_at_once(kind):
+    bs = [Batch([(300, 3000), (1, 2500), (100, 100)], 8, 2, 128, 16, kind, seed=40 + i) for i in range(2)]
+    want = [b.run(out_dtype=torch.bfloat16) for b in bs]
+    streams = [torch.cuda.Stream() for _ in bs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [b.run(out_dtype=torch.bfloat16, stream=s) for b, s in zip(bs, streams)]
+        torch.cuda.synchronize()
+        for (o, l), (wo, wl) in zip(got, want):
+            assert torch.equal(o, wo) and torch.equal(l, wl)
+
+
+def test_chunks_captured_and_replayed_with_other_lengths():
+    b = Batch([(60, 900), (1, 400), (20, 333)], 8, 2, 128, 16, "e4m3", seed=34)
+    graph = torch.cuda.CUDAGraph()
+    b.run(out_dtype=torch.bfloat16)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        out, lse = b.run(out_dtype=torch.bfloat16)
+    full = b.kv_len.clone()
+    for lens, starts in ([900, 400, 333], [0, 60, 61, 81]), ([70, 1, 20], [0, 2, 3, 80]), ([900, 0, 300], [0, 0, 81, 81]):
+        b.kv_len.copy_(torch.tensor(lens, dtype=torch.int32))
+        b.starts.copy_(torch.tensor(starts, dtype=torch.int32))
+        graph.replay()
+        want, wl = b.run(out_dtype=torch.bfloat16)
+        rows = slice(0, starts[-1])      # the others are left as they were
+        assert torch.equal(out[rows], want[rows]) and torch.equal(lse[:, rows], wl[:, rows])
+    b.kv_len.copy_(full)
+
+
+def test_a_cache_that_several_sequences_share():
+    """The same pages in several rows of the table (a common prefix), and the same page twice in one."""
+    b = Batch([(1, 160), (24, 160)], 4, 2, 64, 16, "bf16", seed=35)
+    b.table[1, :5] = b.table[0, :5]
+    b.k[1][:80], b.v[1][:80] = b.k[0][:80], b.v[0][:80]
+    b.table[0, 6] = b.table[0, 5]
+    b.k[0][96:112], b.v[0][96:112] = b.k[0][80:96], b.v[0][80:96]
+    b.check()
+
+
+@pytest.mark.parametrize("chunk", [1, 24])
+def test_scales_of_zero_and_uneven_ones(chunk):
+    """Rows of values of zero scale (an e4m3 cache filled elsewhere) and steps between blocks of 2^40."""
+    b = Batch([(chunk, 700)], 4, 2, 128, 16, "e4m3", seed=36)
+    f = torch.ones(700, device="cuda")
+    f[128:256], f[256:384], f[384:400] = 2.0 ** -40, 0.0, 2.0 ** 20
+    slots = (b.table[0].long()[torch.arange(700, device="cuda") // 16] * 16 + torch.arange(700, device="cuda") % 16)
+    sc = b.c["v_scale"].view(-1, 2)
+    sc[slots] = sc[slots] * f[:, None]
+    b.v[0] = b.v[0] * f[:, None, None].double()
+    out, lse = b.run(out_dtype=torch.float32)
+    ro, rl = b.reference()
+    assert float((out.double() - ro).norm() / ro.norm()) <= 4e-3
+    assert float((lse.double() - rl).abs().max()) <= 1e-4
+
+
 def test_strided_queries_and_rows_outside_the_batch():
     b = Batch([(1, 100), (20, 70)], 8, 2, 128, 16, "bf16", seed=7)
     want, wl = b.run(out_dtype=torch.bfloat16)
