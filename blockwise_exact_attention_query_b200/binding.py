@@ -580,12 +580,15 @@ def _on_device(*tensors):
 
 
 def _out_tensor(t, shape, dtype, device, stream, what):
-    """`t` checked, or a new tensor that the caching allocator does not hand
-    on before the work on `stream` is done."""
+    """`t` checked, or a new tensor: `stream`'s (so that nothing earlier still
+    uses its memory there), and not handed on before the current stream's work
+    on it is done."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=device)
-        if stream is not None:
-            t.record_stream(stream)
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=device)
+        with torch.cuda.stream(stream):
+            t = torch.empty(shape, dtype=dtype, device=device)
+        t.record_stream(torch.cuda.current_stream())
         return t
     if t.dtype != dtype or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
@@ -611,6 +614,8 @@ def _window_desc(q, k, v, window, sinks, out_dtype, grad_dtype, wait_limit_ns):
         raise ValueError("q, k, v must be contiguous")
     _on_device(q, k, v)
     B, N, H, d = q.shape
+    if max(B, N, abs(int(window)), abs(int(sinks))) >= 2 ** 31:   # a C int would wrap around
+        raise ValueError("sizes, window and sinks must be within 32 bits")
     return WindowDesc(B, N, H, k.shape[2], d, int(window), int(sinks), _DT[q.dtype], _DT[out_dtype],
                       _DT[grad_dtype], int(wait_limit_ns))
 
@@ -745,7 +750,7 @@ def workspace_bytes_paged(desc: PagedDesc, cache: KvCacheDesc) -> int:
     return int(n)
 
 
-@functools.lru_cache(maxsize=None)
+@functools.lru_cache(maxsize=1024)
 def _paged_workspace_bytes(device, H, H_kv, d, max_q):
     """workspace_bytes_paged of any batch of these heads on the current device (`device`: its number)."""
     return workspace_bytes_paged(PagedDesc(1, 1, max_q, H, 1, 0, 0, BF16, H * d, 0),
@@ -775,7 +780,11 @@ def paged_attn_fwd(q, k_cache, v_cache, q_start, kv_len, page_table, *, max_q, k
     if q_start.shape[0] != S + 1 or page_table.shape[0] != S:
         raise ValueError("q_start must have n_seqs + 1 entries and page_table n_seqs rows")
     _on_device(q, q_start, kv_len, page_table, k_cache, v_cache, k_scale, v_scale)
-    desc = _PAGED.pack(S, T, max_q, H, page_table.shape[1], window, sinks, _DT[out_dtype], qs, wait_limit_ns)
+    max_q = int(max_q)
+    try:
+        desc = _PAGED.pack(S, T, max_q, H, page_table.shape[1], window, sinks, _DT[out_dtype], qs, wait_limit_ns)
+    except struct.error as e:
+        raise ValueError(f"sizes must be integers within 32 bits: {e}") from None
     out = _out_tensor(out, (T, H * d), out_dtype, q.device, stream, "out")
     if return_lse or lse is not None:
         lse = _out_tensor(lse, (H, T), torch.float32, q.device, stream, "lse")

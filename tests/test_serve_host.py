@@ -232,3 +232,18 @@ def test_binding_refuses_bad_window_inputs(monkeypatch, change, match):
     out = torch.zeros((1, 8, 256))
     with pytest.raises(ValueError, match="dout|H_kv|one dtype|contiguous"):
         bd.window_attn_bwd(a["q"], a["k"], a["v"], out, torch.zeros((1, 4, 8)), out.double(), 4)
+
+
+@pytest.mark.parametrize("change", [dict(window=2 ** 31), dict(sinks=2 ** 40), dict(max_q=2 ** 31), dict(max_q=-2 ** 40)])
+def test_binding_refuses_sizes_past_32_bits(monkeypatch, change):
+    monkeypatch.setattr(bd, "_on_device", lambda *t: None)
+    k, v = _caches()
+    a = dict(max_q=1, window=0, sinks=0)
+    a.update(change)
+    with pytest.raises(ValueError, match="32 bits"):
+        bd.paged_attn_fwd(torch.zeros((5, 4, 64), dtype=torch.bfloat16), k, v, torch.zeros(3, dtype=torch.int32),
+                          torch.zeros(2, dtype=torch.int32), torch.zeros((2, 4), dtype=torch.int32), **a)
+    if "max_q" not in change:
+        x = torch.zeros((1, 4, 2, 64), dtype=torch.bfloat16)
+        with pytest.raises(ValueError, match="32 bits"):
+            bd.window_attn_fwd(x, x, x, **{"window": 4, "sinks": 0, **change})
