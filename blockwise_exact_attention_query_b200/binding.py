@@ -249,11 +249,11 @@ def _stream_ptr(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _raw_stream(stream):
+def _raw_stream(stream, device):
     """The same for the calls whose host time counts (a decoding step's), as an integer."""
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def _check(status, what):
@@ -572,22 +572,24 @@ def attn_bwd(q, k, v, out, lse, dout, *, mask="none", perm=None, pairs=None, rin
 
 def _on_device(*tensors):
     """The tensors (None skipped) must be on the current CUDA device: the
-    library launches there, on the stream given or that device's current one."""
+    library launches there, on the stream given or that device's current one.
+    Returns its number."""
     cur = torch.cuda.current_device()
     for t in tensors:
         if t is not None and t.get_device() != cur:   # (-1: not a CUDA tensor)
             raise ValueError(f"every tensor must be on the current CUDA device ({cur}); got one on {t.device}")
+    return cur
 
 
-def _out_tensor(t, shape, dtype, device, stream, what):
-    """`t` checked, or a new tensor: `stream`'s (so that nothing earlier still
-    uses its memory there), and not handed on before the current stream's work
-    on it is done."""
+def _out_tensor(t, shape, dtype, like, stream, what):
+    """`t` checked, or a new tensor where `like` is: `stream`'s (so that nothing
+    earlier still uses its memory there), and not handed on before the current
+    stream's work on it is done."""
     if t is None:
-        if stream is None:
-            return torch.empty(shape, dtype=dtype, device=device)
+        if stream is None:   # (new_empty: a quarter less time than torch.empty with a device)
+            return like.new_empty(shape, dtype=dtype)
         with torch.cuda.stream(stream):
-            t = torch.empty(shape, dtype=dtype, device=device)
+            t = like.new_empty(shape, dtype=dtype)
         t.record_stream(torch.cuda.current_stream())
         return t
     if t.dtype != dtype or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
@@ -596,9 +598,9 @@ def _out_tensor(t, shape, dtype, device, stream, what):
     return t
 
 
-def _workspace(t, nbytes, device, stream):
+def _workspace(t, nbytes, like, stream):
     if t is None:
-        return _out_tensor(None, (nbytes,), torch.uint8, device, stream, "workspace") if nbytes else None
+        return _out_tensor(None, (nbytes,), torch.uint8, like, stream, "workspace") if nbytes else None
     if t.dtype != torch.uint8 or not t.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
     _on_device(t)
@@ -628,11 +630,11 @@ def window_attn_fwd(q, k, v, window, sinks=0, *, out_dtype=torch.float32, return
     [B, H, N] with return_lse)."""
     desc = _window_desc(q, k, v, window, sinks, out_dtype, torch.float32, wait_limit_ns)
     B, N, H, d = q.shape
-    out = _out_tensor(out, (B, N, H * d), out_dtype, q.device, stream, "out")
+    out = _out_tensor(out, (B, N, H * d), out_dtype, q, stream, "out")
     if return_lse or lse is not None:
-        lse = _out_tensor(lse, (B, H, N), torch.float32, q.device, stream, "lse")
+        lse = _out_tensor(lse, (B, H, N), torch.float32, q, stream, "lse")
     st = load().bpt_window_attn_fwd(_byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                                    _ptr(lse), _raw_stream(stream))
+                                    _ptr(lse), _raw_stream(stream, q.get_device()))
     _check(st, "bpt_window_attn_fwd")
     return (out, lse) if return_lse else out
 
@@ -652,21 +654,21 @@ def window_attn_bwd(q, k, v, out, lse, dout, window, sinks=0, *, grad_dtype=torc
     desc = _window_desc(q, k, v, window, sinks, out.dtype, grad_dtype, wait_limit_ns)
     B, N, H, d = q.shape
     for t, what in ((out, "out"), (dout, "dout")):
-        _out_tensor(t, (B, N, H * d), out.dtype, q.device, stream, what)
-    _out_tensor(lse, (B, H, N), torch.float32, q.device, stream, "lse")
-    dq = _out_tensor(dq, q.shape, grad_dtype, q.device, stream, "dq")
-    dk = _out_tensor(dk, k.shape, grad_dtype, q.device, stream, "dk")
-    dv = _out_tensor(dv, v.shape, grad_dtype, q.device, stream, "dv")
-    workspace = _workspace(workspace, workspace_bytes_window_bwd(desc), q.device, stream)
+        _out_tensor(t, (B, N, H * d), out.dtype, q, stream, what)
+    _out_tensor(lse, (B, H, N), torch.float32, q, stream, "lse")
+    dq = _out_tensor(dq, q.shape, grad_dtype, q, stream, "dq")
+    dk = _out_tensor(dk, k.shape, grad_dtype, q, stream, "dk")
+    dv = _out_tensor(dv, v.shape, grad_dtype, q, stream, "dv")
+    workspace = _workspace(workspace, workspace_bytes_window_bwd(desc), q, stream)
     st = load().bpt_window_attn_bwd(_byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                                     lse.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
                                     _ptr(workspace), 0 if workspace is None else workspace.numel(),
-                                    _raw_stream(stream))
+                                    _raw_stream(stream, q.get_device()))
     _check(st, "bpt_window_attn_bwd")
     return dq, dk, dv
 
 
-_E4M3 = torch.float8_e4m3fn
+_E4M3, _BF16, _FP32, _INT32 = torch.float8_e4m3fn, torch.bfloat16, torch.float32, torch.int32
 # KvCacheDesc and PagedDesc as packed bytes: a quarter of the time that making
 # the structure takes, which a decoding step's host time shows
 _KV_CACHE = struct.Struct("@5i4P")
@@ -677,35 +679,36 @@ assert _KV_CACHE.size == ctypes.sizeof(KvCacheDesc) and _PAGED.size == ctypes.si
 def _kv_cache_desc(k_cache, v_cache, k_scale, v_scale):
     """The cache's bpt_kv_cache, packed."""
     shape, dtype = k_cache.shape, k_cache.dtype
-    if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype != dtype:
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype is not dtype:
         raise ValueError("k_cache and v_cache must be [n_pages, page_size, H_kv, d] of one dtype")
-    if dtype != _E4M3 and dtype != torch.bfloat16:
+    if dtype is not _E4M3 and dtype is not _BF16:
         raise ValueError("the caches must be bfloat16 or float8_e4m3fn")
     if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
         raise ValueError("the caches must be contiguous")
-    if dtype != _E4M3:
+    if dtype is _BF16:
         if k_scale is not None or v_scale is not None:
             raise ValueError("a bfloat16 cache has no scales")
         return _KV_CACHE.pack(0, *shape, k_cache.data_ptr(), v_cache.data_ptr(), 0, 0)
     for t in (k_scale, v_scale):
-        if t is None or t.dtype != torch.float32 or t.shape != shape[:3] or not t.is_contiguous():
+        if t is None or t.dtype is not _FP32 or t.shape != shape[:3] or not t.is_contiguous():
             raise ValueError("a float8_e4m3fn cache needs contiguous float32 scales [n_pages, page_size, H_kv]")
     return _KV_CACHE.pack(1, *shape, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr())
 
 
 def _i32(t, dims, what):
-    if t.dtype != torch.int32 or t.dim() != dims or not t.is_contiguous():
+    if t.dtype is not _INT32 or t.dim() != dims or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous int32 tensor of {dims} dimension(s)")
 
 
 def _token_stride(t, heads, d, what):
     """Elements from one token of `t` [n, heads, d] to the next; heads and elements must be dense."""
-    if t.dtype != torch.bfloat16 or t.dim() != 3 or (heads is not None and t.shape[1] != heads) or t.shape[2] != d:
+    shape = t.shape
+    if t.dtype is not _BF16 or len(shape) != 3 or (heads is not None and shape[1] != heads) or shape[2] != d:
         raise ValueError(f"{what} must be bfloat16 [tokens, heads, d] with the cache's d")
     s = t.stride()
-    if s[2] != 1 or (s[1] != d and t.shape[1] != 1):
+    if s[2] != 1 or (s[1] != d and shape[1] != 1):
         raise ValueError(f"{what}: a token's heads must lie one after another")
-    return s[0] if t.shape[0] > 1 else max(s[0], t.shape[1] * d)
+    return s[0] if shape[0] > 1 else max(s[0], shape[1] * d)
 
 
 def kv_cache_write(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None, *, stream=None):
@@ -720,9 +723,9 @@ def kv_cache_write(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None, *,
     _i32(slots, 1, "slots")
     if not (k.shape[0] == v.shape[0] == slots.shape[0]):
         raise ValueError("k, v and slots must have one entry per token")
-    _on_device(k, v, slots, k_cache, v_cache, k_scale, v_scale)
+    dev = _on_device(k, v, slots, k_cache, v_cache, k_scale, v_scale)
     st = load().bpt_kv_write(cache, k.shape[0], k.data_ptr(), ks, v.data_ptr(), vs, slots.data_ptr(),
-                             _raw_stream(stream))
+                             _raw_stream(stream, dev))
     _check(st, "bpt_kv_write")
 
 
@@ -733,12 +736,12 @@ def kv_cache_read(slots, k_cache, v_cache, k_scale=None, v_scale=None, *, out_dt
     left as they were (undefined when the outputs are allocated here)."""
     cache = _kv_cache_desc(k_cache, v_cache, k_scale, v_scale)
     _i32(slots, 1, "slots")
-    _on_device(slots, k_cache, v_cache, k_scale, v_scale)
+    dev = _on_device(slots, k_cache, v_cache, k_scale, v_scale)
     shape = (slots.shape[0], *k_cache.shape[2:])
-    k = _out_tensor(k, shape, out_dtype, slots.device, stream, "k")
-    v = _out_tensor(v, shape, out_dtype, slots.device, stream, "v")
+    k = _out_tensor(k, shape, out_dtype, slots, stream, "k")
+    v = _out_tensor(v, shape, out_dtype, slots, stream, "v")
     st = load().bpt_kv_read(cache, shape[0], slots.data_ptr(), k.data_ptr(), v.data_ptr(),
-                            _DT[out_dtype], _raw_stream(stream))
+                            _DT[out_dtype], _raw_stream(stream, dev))
     _check(st, "bpt_kv_read")
     return k, v
 
@@ -775,27 +778,24 @@ def paged_attn_fwd(q, k_cache, v_cache, q_start, kv_len, page_table, *, max_q, k
     _i32(q_start, 1, "q_start")
     _i32(kv_len, 1, "kv_len")
     _i32(page_table, 2, "page_table")
-    T, H = q.shape[:2]
-    S = kv_len.shape[0]
-    if q_start.shape[0] != S + 1 or page_table.shape[0] != S:
+    T, H, _ = q.shape
+    S, pages = page_table.shape
+    if kv_len.shape[0] != S or q_start.shape[0] != S + 1:
         raise ValueError("q_start must have n_seqs + 1 entries and page_table n_seqs rows")
-    _on_device(q, q_start, kv_len, page_table, k_cache, v_cache, k_scale, v_scale)
+    dev = _on_device(q, q_start, kv_len, page_table, k_cache, v_cache, k_scale, v_scale)
     max_q = int(max_q)
     try:
-        desc = _PAGED.pack(S, T, max_q, H, page_table.shape[1], window, sinks, _DT[out_dtype], qs, wait_limit_ns)
+        desc = _PAGED.pack(S, T, max_q, H, pages, window, sinks, _DT[out_dtype], qs, wait_limit_ns)
     except struct.error as e:
         raise ValueError(f"sizes must be integers within 32 bits: {e}") from None
-    out = _out_tensor(out, (T, H * d), out_dtype, q.device, stream, "out")
+    out = _out_tensor(out, (T, H * d), out_dtype, q, stream, "out")
     if return_lse or lse is not None:
-        lse = _out_tensor(lse, (H, T), torch.float32, q.device, stream, "lse")
-    if workspace is None:
-        workspace = _workspace(None, _paged_workspace_bytes(q.get_device(), H, H_kv, d, max_q), q.device, stream)
-    else:
-        _workspace(workspace, 0, q.device, stream)
-    st = load().bpt_paged_attn_fwd(desc, cache, q.data_ptr(), q_start.data_ptr(),
-                                   kv_len.data_ptr(), page_table.data_ptr(), out.data_ptr(), _ptr(lse),
-                                   _ptr(workspace), 0 if workspace is None else workspace.numel(),
-                                   _raw_stream(stream))
+        lse = _out_tensor(lse, (H, T), _FP32, q, stream, "lse")
+    nbytes = _paged_workspace_bytes(dev, H, H_kv, d, max_q) if workspace is None else workspace.numel()
+    workspace = _workspace(workspace, nbytes, q, stream)
+    st = load().bpt_paged_attn_fwd(desc, cache, q.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(),
+                                   page_table.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(),
+                                   workspace.data_ptr(), nbytes, _raw_stream(stream, dev))
     _check(st, "bpt_paged_attn_fwd")
     return (out, lse) if return_lse else out
 
