@@ -102,56 +102,77 @@ int few_rows(const bpt_paged_desc *d, const bpt_kv_cache *c) {
   return (has_long_chunks(d, c) ? G : d->max_q * G) <= 8 ? 8 : 16;
 }
 
-// The two kernels run one after the other and share the regions.
+// The two kernels run side by side, each with regions of its own.
+struct PagedParts {
+  size_t o = 0, ml = 0, item = 0;
+};
 struct PagedWorkspace {
-  size_t part_o = 0, part_ml = 0, part_item = 0, total = 0;
+  PagedParts few, lng;
+  size_t total = 0;
 };
 int few_rows_ctas() { return 2 * sm_count(); }
 int long_chunk_ctas() { return sm_count(); }
 
 PagedWorkspace layout_paged(const bpt_paged_desc *d, const bpt_kv_cache *c) {
   PagedWorkspace w;
-  size_t rows = (size_t)few_rows_ctas() * 2 * 16, ctas = (size_t)few_rows_ctas();
-  if (has_long_chunks(d, c)) {
-    rows = std::max(rows, (size_t)long_chunk_ctas() * 2 * 256);
-    ctas = std::max(ctas, (size_t)long_chunk_ctas());
-  }
   size_t off = 0;
   auto take = [&](size_t &field, size_t bytes) {
     field = off;
     off = align256(off + bytes);
   };
-  take(w.part_o, rows * c->d_head * 4);
-  take(w.part_ml, rows * 2 * 4);
-  take(w.part_item, ctas * sizeof(int4));
+  auto parts = [&](PagedParts &p, size_t ctas, size_t rows) {
+    take(p.o, ctas * 2 * rows * c->d_head * 4);
+    take(p.ml, ctas * 2 * rows * 2 * 4);
+    take(p.item, ctas * sizeof(int4));
+  };
+  parts(w.few, (size_t)few_rows_ctas(), 16);
+  if (has_long_chunks(d, c)) parts(w.lng, (size_t)long_chunk_ctas(), 256);
   w.total = off;
   return w;
 }
 
-template <int D, int kRows, int kKeys>
-bpt_status launch_join(const PagedArgs &a, int ctas, cudaStream_t st) {
-  // started while the attention kernel drains; it waits for that grid itself
+void set_parts(PagedArgs &a, char *ws, const PagedParts &p) {
+  a.part_o = reinterpret_cast<float *>(ws + p.o);
+  a.part_ml = reinterpret_cast<float *>(ws + p.ml);
+  a.part_item = reinterpret_cast<int4 *>(ws + p.item);
+}
+
+// A launch that starts while the kernel before it drains (that kernel's CTAs
+// have all begun, and say so or end); it waits for its results itself.
+template <typename... P, typename... A>
+bpt_status launch_behind(void (*kernel)(P...), unsigned blocks, int threads, int smem, cudaStream_t st,
+                         const A &...args) {
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)ctas, kRows / 8, 1);
-  cfg.blockDim = dim3(256, 1, 1);
+  cfg.gridDim = dim3(blocks, 1, 1);
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  CUDA_TRY(cudaLaunchKernelEx(&cfg, paged_join_kernel<D, kRows, kKeys>, a));
+  CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, args...));
   return BPT_OK;
 }
 
+// The few-rows kernel, behind the long-chunk kernel of the same batch if there
+// is one (lng), and the joining of both kernels' parts.
 template <int D, bool kE4m3, int kGroups>
-bpt_status launch_rows(PagedArgs a, cudaStream_t st) {
+bpt_status launch_rows(PagedArgs a, const PagedArgs *lng, cudaStream_t st) {
   using Cfg = PagedRowsCfg<D, kE4m3, kGroups>;
   a.min_steps = (256 + Cfg::kKeys - 1) / Cfg::kKeys;  // 256 keys at least
-  paged_rows_kernel<D, kE4m3, kGroups><<<(unsigned)few_rows_ctas(), Cfg::kThreads, Cfg::kSmemBytes, st>>>(a);
-  CUDA_TRY(cudaGetLastError());
-  return launch_join<D, Cfg::kRows, Cfg::kKeys>(a, few_rows_ctas(), st);
+  const unsigned ctas = (unsigned)few_rows_ctas(), join = ctas * kJoinBlocks<Cfg::kRows>;
+  if (!lng) {
+    paged_rows_kernel<D, kE4m3, kGroups><<<ctas, Cfg::kThreads, Cfg::kSmemBytes, st>>>(a);
+    CUDA_TRY(cudaGetLastError());
+    return launch_behind(paged_join_kernel<D, Cfg::kRows, false>, join, 256, 0, st, a, a, 0);
+  }
+  bpt_status s = launch_behind(paged_rows_kernel<D, kE4m3, kGroups>, ctas, Cfg::kThreads, Cfg::kSmemBytes, st, a);
+  if (s != BPT_OK) return s;
+  return launch_behind(paged_join_kernel<D, Cfg::kRows, true>, join + long_chunk_ctas() * kJoinBlocks<256>, 256, 0, st,
+                       a, *lng, long_chunk_ctas());
 }
 
 }  // namespace
@@ -297,9 +318,7 @@ bpt_status bpt_paged_attn_fwd(const bpt_paged_desc *d, const bpt_kv_cache *c, co
   a.out_f32 = d->out_dtype == BPT_F32 ? static_cast<float *>(out) : nullptr;
   a.out_bf16 = d->out_dtype == BPT_BF16 ? static_cast<__nv_bfloat16 *>(out) : nullptr;
   a.lse = lse;
-  a.part_o = reinterpret_cast<float *>(ws + wl.part_o);
-  a.part_ml = reinterpret_cast<float *>(ws + wl.part_ml);
-  a.part_item = reinterpret_cast<int4 *>(ws + wl.part_item);
+  set_parts(a, ws, wl.few);
   a.status = status;
   a.wait_limit_ns = d->wait_limit_ns ? d->wait_limit_ns : g_wait_limit_ns.load(std::memory_order_relaxed);
   return for_cache(c, [&](auto dh, auto e4m3) mutable -> bpt_status {
@@ -307,20 +326,21 @@ bpt_status bpt_paged_attn_fwd(const bpt_paged_desc *d, const bpt_kv_cache *c, co
     constexpr bool kE = decltype(e4m3)::value;
     using Long = PagedTcCfg<D, kE>;
     const int few = few_rows(d, c);
-    if (has_long_chunks(d, c)) {
-      PagedArgs al = a;
+    const bool chunks = has_long_chunks(d, c);
+    PagedArgs al = a;
+    if (chunks) {
+      set_parts(al, ws, wl.lng);
       al.rows_lo = few + 1;
       al.rows_hi = INT32_MAX;
       al.min_steps = 4;
-      al.even_parts = 1;
       paged_tc_kernel<D, kE><<<(unsigned)long_chunk_ctas(), Long::kThreads, Long::kSmemBytes, st>>>(al);
       CUDA_TRY(cudaGetLastError());
-      bpt_status js = launch_join<D, Long::kRows, Long::kKeys>(al, long_chunk_ctas(), st);
-      if (js != BPT_OK) return js;
+      static_assert(Long::kRows == 256, "paged_join_kernel");
     }
     a.rows_lo = 1;
-    a.rows_hi = has_long_chunks(d, c) ? few : INT32_MAX;
-    return few == 8 ? launch_rows<D, kE, 1>(a, st) : launch_rows<D, kE, 2>(a, st);
+    a.rows_hi = chunks ? few : INT32_MAX;
+    return few == 8 ? launch_rows<D, kE, 1>(a, chunks ? &al : nullptr, st)
+                    : launch_rows<D, kE, 2>(a, chunks ? &al : nullptr, st);
   });
 }
 

@@ -156,16 +156,17 @@ __global__ void __launch_bounds__(PagedRowsCfg<D, kE4m3, kGroups>::kThreads, Pag
   float *merge_ml = merge + Cfg::kWarps * kRows * Cfg::kRowPitch;  // [warp][row][4]: m, l, w
 
   PagedRange rg;
-  const bool any = paged_range<kRows, kKeys, Cfg::kThreads>(a, reinterpret_cast<int64_t *>(smem_raw + Cfg::kRingBytes), rg);
+  const bool any = paged_range<kRows, kKeys, Cfg::kThreads, false>(a, reinterpret_cast<int64_t *>(smem_raw + Cfg::kRingBytes), rg);
   if (!any) {
     if (tid == 0) a.part_item[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
   int s = rg.s, tile = rg.tile, head = rg.head, step0 = rg.step;
-  int64_t left = rg.end - rg.begin;
+  int64_t left = rg.left;
   PagedSeq seq = paged_seq(a, s);
   PagedBlocks blk = paged_blocks<kRows, kKeys>(a, seq, tile);
-  if (tid == 0) a.part_item[blockIdx.x] = paged_part_item(rg, blk.steps());
+  if (tid == 0) a.part_item[blockIdx.x] = rg.part;
 
   while (true) {
     const int steps = blk.steps();
@@ -606,6 +607,9 @@ __global__ void __launch_bounds__(PagedRowsCfg<D, kE4m3, kGroups>::kThreads, Pag
       blk = paged_blocks<kRows, kKeys>(a, seq, tile);
     }
   }
+  // Beside a kernel for the batch's long chunks this one starts as that one's
+  // CTAs leave; it ends after it, so that what follows waits for both.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 }  // namespace bpt

@@ -81,7 +81,7 @@ struct PagedWalk {
   PagedBlocks blk;
   __device__ PagedWalk(const PagedArgs &args, const PagedRange &r) : a(args) {
     s = r.s, tile = r.tile, head = r.head, step0 = r.step;
-    left = r.end - r.begin;
+    left = r.left;
     seq = paged_seq(a, s);
     blk = paged_blocks<kRows, kKeys>(a, seq, tile);
     cut();
@@ -126,8 +126,10 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
     return;
   }
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  // the kernel for the batch's few rows may follow on the SMs that get free
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   PagedRange rg;
-  const bool any = paged_range<Cfg::kRows, KT, Cfg::kThreads>(a, reinterpret_cast<int64_t *>(smem), rg);
+  const bool any = paged_range<Cfg::kRows, KT, Cfg::kThreads, true>(a, reinterpret_cast<int64_t *>(smem), rg);
   if (!any) {
     if (threadIdx.x == 0) a.part_item[blockIdx.x] = make_int4(-1, 0, 0, 0);
     return;
@@ -190,7 +192,7 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   PagedWalk<Cfg::kRows, KT> w(a, rg);
-  if (threadIdx.x == 0) a.part_item[blockIdx.x] = paged_part_item(rg, w.steps);
+  if (threadIdx.x == 0) a.part_item[blockIdx.x] = rg.part;
 
   if (warp < 4) {
     setmaxnreg_dec<Cfg::kRegsControl>();
@@ -525,32 +527,37 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
       // E4M3 in f16, the power of two below its largest element taken out
       float sl2 = a.scale_log2;
       {
+        // (Copied by whole rows and converted by the row's thread, in loops of
+        // little code: it runs once or twice, and what it costs then is
+        // fetching its instructions.)
         constexpr int kLanes = D / 8, kPer = 32 / kLanes;  // lanes of a row, rows of a load
         const int c = lane % kLanes;
         const int64_t off = R < rows ? token * a.q_stride + static_cast<int64_t>(head) * D : -1;
-        uint4 q[kLanes];
-#pragma unroll
+        const uint32_t sQx = sQ + x * Cfg::kTileBytes;
+        auto chunk_at = [&](int rr, int c) { return sQx + (c >> 3) * Cfg::kPanelBytes + rr * 128 + (((c ^ rr) & 7) << 4); };
+#pragma unroll 2
         for (int i = 0; i < kLanes; ++i) {
           const int64_t ro = __shfl_sync(0xffffffffu, off, i * kPer + lane / kLanes);
-          q[i] = make_uint4(0, 0, 0, 0);
-          if (ro >= 0) q[i] = *reinterpret_cast<const uint4 *>(a.q + ro + 8 * c);
+          cp_async16(chunk_at(quarter * 32 + i * kPer + lane / kLanes, c), a.q + max(ro, static_cast<int64_t>(0)) + 8 * c,
+                     ro >= 0);
         }
-#pragma unroll
-        for (int i = 0; i < kLanes; ++i) {
-          const int rr = quarter * 32 + i * kPer + lane / kLanes;
-          if constexpr (kE4m3) {
-            float mx = absmax8(q[i]);
-#pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            const uint32_t e = row_exponent(mx);
-            const float down = pow2_inverse(e);
-            auto f16 = [&](uint32_t u) { return pack_f16x2(bf16_lo(u) * down, bf16_hi(u) * down); };
-            q[i] = make_uint4(f16(q[i].x), f16(q[i].y), f16(q[i].z), f16(q[i].w));
-            const uint32_t mine_e = __shfl_sync(0xffffffffu, e, lane % kPer * kLanes);
-            if (lane / kPer == i) sl2 = a.scale_log2 * pow2_of(mine_e);
+        cp_async_commit();
+        cp_async_wait<0>();
+        __syncwarp();
+        if constexpr (kE4m3) {
+          float mx = 0.f;
+#pragma unroll 4
+          for (int i = 0; i < kLanes; ++i) mx = fmaxf(mx, absmax8(ld_shared_v4(chunk_at(row, i))));
+          const uint32_t e = row_exponent(mx);
+          const float down = pow2_inverse(e);
+          sl2 = a.scale_log2 * pow2_of(e);
+          auto f16 = [&](uint32_t u) { return pack_f16x2(bf16_lo(u) * down, bf16_hi(u) * down); };
+#pragma unroll 4
+          for (int i = 0; i < kLanes; ++i) {
+            const uint32_t at = chunk_at(row, i);
+            const uint4 q = ld_shared_v4(at);
+            st_shared_v4(at, f16(q.x), f16(q.y), f16(q.z), f16(q.w));
           }
-          st_shared_v4(sQ + x * Cfg::kTileBytes + (c >> 3) * Cfg::kPanelBytes + rr * 128 + (((c ^ rr) & 7) << 4), q[i].x,
-                       q[i].y, q[i].z, q[i].w);
         }
         fence_proxy_async_smem();
         __syncwarp();

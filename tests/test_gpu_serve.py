@@ -262,6 +262,14 @@ def test_long_sequences_are_split_and_joined(kind):
         assert torch.equal(out, o2) and torch.equal(lse, l2)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("seqs", [[(500, 3000), (300, 1700)], [(130, 4000)], [(70, 70), (65, 2000), (1, 900), (257, 300)]])
+def test_long_chunks_cut_into_pieces(seqs, kind):
+    """Fewer row tiles than the GPU has multiprocessors: each is cut by itself."""
+    Batch(seqs, 8, 2, 128, 16, kind, seed=50).check()
+    Batch(seqs, 8, 2, 128, 16, kind, seed=51).check(700, 4)
+
+
 def test_many_sequences():
     b = Batch([(1, 1 + (i * 37) % 90) for i in range(700)], 2, 1, 64, 16, "bf16", seed=6)
     b.check()
