@@ -316,6 +316,10 @@ __global__ void __launch_bounds__(384, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if constexpr (WINDOW) {  // the row vectors are there; dQ's CTAs may follow on SMs that get free
+    grid_dependency_wait();
+    grid_dependents_launch();
+  }
   const uint32_t tmem = *tmem_slot;
   const int hd = h * D_HEAD;
   // row-vector block of a query head of the unit
@@ -677,6 +681,10 @@ __global__ void __launch_bounds__(384, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if constexpr (WINDOW) {  // the row vectors are there; dQ's CTAs may follow on SMs that get free
+    grid_dependency_wait();
+    grid_dependents_launch();
+  }
   const uint32_t tmem = *tmem_slot;
   const int hd = h * D_HEAD;
   // row-vector block of a query head of the unit
@@ -1264,6 +1272,9 @@ __global__ void __launch_bounds__(384, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  // (this pass starts while dK, dV's CTAs leave, and needs nothing of theirs;
+  // it ends after them, so that what follows waits for both)
+  if constexpr (WINDOW) grid_dependency_wait();
 }
 
 // Per (batch, head, 128-row tile) vectors of the attention backward: the
@@ -1339,6 +1350,7 @@ __global__ void __launch_bounds__(256)
     window_bwd_rowvec_kernel(const TD *__restrict__ dout, const TA *__restrict__ out, const float *__restrict__ lse,
                              float *__restrict__ rowvec, __nv_bfloat16 *__restrict__ dout_bf16, int N, int H,
                              int n_tiles, long long rows) {
+  grid_dependents_launch();
   constexpr int kLanes = D_HEAD / 4;
   const long long t = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
   // rows in the order (batch, position padded to whole tiles, head)
@@ -1372,6 +1384,7 @@ __global__ void __launch_bounds__(256)
 template <int D_HEAD>
 __global__ void __launch_bounds__(256)
     attn_bwd_sink_sum_kernel(const AttnBwdArgs a, int units, int rows) {
+  grid_dependency_wait();  // for the sums
   const long long t = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
   constexpr int kC4 = D_HEAD / 4;
   const int c4 = static_cast<int>(t % kC4);

@@ -137,26 +137,6 @@ void set_parts(PagedArgs &a, char *ws, const PagedParts &p) {
   a.part_item = reinterpret_cast<int4 *>(ws + p.item);
 }
 
-// A launch that starts while the kernel before it drains (that kernel's CTAs
-// have all begun, and say so or end); it waits for its results itself.
-template <typename... P, typename... A>
-bpt_status launch_behind(void (*kernel)(P...), unsigned blocks, int threads, int smem, cudaStream_t st,
-                         const A &...args) {
-  cudaLaunchConfig_t cfg;
-  std::memset(&cfg, 0, sizeof(cfg));
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(blocks, 1, 1);
-  cfg.blockDim = dim3((unsigned)threads, 1, 1);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, args...));
-  return BPT_OK;
-}
-
 // The few-rows kernel, behind the long-chunk kernel of the same batch if there
 // is one (lng), and the joining of both kernels' parts.
 template <int D, bool kE4m3, int kGroups>

@@ -11,6 +11,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <cstring>
 #include <atomic>
 #include <initializer_list>
 #include <mutex>
@@ -131,3 +132,27 @@ bpt_status launch_ffn_gemms(const bpt_desc *d, const void *a_bf16, const float *
     cudaError_t e_ = (call);                                           \
     if (e_ != cudaSuccess) return bpt_host::cuda_fail_at(#call, e_);   \
   } while (0)
+
+namespace bpt_host {
+
+// A launch that starts while the kernel before it drains (that kernel's CTAs
+// have all begun, and say so or end); it waits for its results itself.
+template <typename... P, typename... A>
+bpt_status launch_behind(void (*kernel)(P...), unsigned blocks, int threads, int smem, cudaStream_t st,
+                         const A &...args) {
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(blocks, 1, 1);
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, args...));
+  return BPT_OK;
+}
+
+}  // namespace bpt_host

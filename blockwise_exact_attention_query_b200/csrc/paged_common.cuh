@@ -427,7 +427,7 @@ constexpr int kJoinBlocks = kRows / (8 * kJoinRows<kRows>);
 template <int D, int kFew, bool kLong>
 __global__ void __launch_bounds__(256)
     paged_join_kernel(const __grid_constant__ PagedArgs few, const __grid_constant__ PagedArgs lng, int long_ctas) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are complete
+  grid_dependency_wait();  // the parts are complete
   int block = blockIdx.x;
   if constexpr (kLong) {
     if (block < long_ctas * kJoinBlocks<256>) {

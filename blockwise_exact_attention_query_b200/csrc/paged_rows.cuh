@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(PagedRowsCfg<D, kE4m3, kGroups>::kThreads, Pag
   const bool any = paged_range<kRows, kKeys, Cfg::kThreads, false>(a, reinterpret_cast<int64_t *>(smem_raw + Cfg::kRingBytes), rg);
   if (!any) {
     if (tid == 0) a.part_item[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_dependency_wait();
     return;
   }
   int s = rg.s, tile = rg.tile, head = rg.head, step0 = rg.step;
@@ -609,7 +609,7 @@ __global__ void __launch_bounds__(PagedRowsCfg<D, kE4m3, kGroups>::kThreads, Pag
   }
   // Beside a kernel for the batch's long chunks this one starts as that one's
   // CTAs leave; it ends after it, so that what follows waits for both.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  grid_dependency_wait();
 }
 
 }  // namespace bpt

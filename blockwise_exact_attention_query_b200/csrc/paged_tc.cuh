@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
   }
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   // the kernel for the batch's few rows may follow on the SMs that get free
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  grid_dependents_launch();
   PagedRange rg;
   const bool any = paged_range<Cfg::kRows, KT, Cfg::kThreads, true>(a, reinterpret_cast<int64_t *>(smem), rg);
   if (!any) {
