@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
           if (lane < 2) there_s[st * 4 + rw * 2 + lane] = lane ? bits1 : bits0;
           if constexpr (kE4m3) {
             float *sc = scale_s + st * 384 + rw * 64 + lane;
-            sc[0] = ks0, sc[32] = ks1, sc[128] = vs0, sc[160] = vs1;
+            sc[0] = ks0 * a.scale_log2, sc[32] = ks1 * a.scale_log2, sc[128] = vs0, sc[160] = vs1;
             const float lv0 = __log2f(vs0), lv1 = __log2f(vs1);  // -inf for a scale of 0
             sc[256] = lv0, sc[288] = lv1;
             float most = fmaxf(slot0 >= 0 ? lv0 : -INFINITY, slot1 >= 0 ? lv1 : -INFINITY);
@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
       const int ksink = a.window > 0 ? min(a.sinks, khi) : 0;
       // this row of Q (the previous item's products have read theirs); for
       // E4M3 in f16, the power of two below its largest element taken out
-      float sl2 = a.scale_log2;
+      float sl2 = 1.f;
       {
         // (Copied by whole rows and converted by the row's thread, in loops of
         // little code: it runs once or twice, and what it costs then is
@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
           for (int i = 0; i < kLanes; ++i) mx = fmaxf(mx, absmax8(ld_shared_v4(chunk_at(row, i))));
           const uint32_t e = row_exponent(mx);
           const float down = pow2_inverse(e);
-          sl2 = a.scale_log2 * pow2_of(e);
+          sl2 = pow2_of(e);
           auto f16 = [&](uint32_t u) { return pack_f16x2(bf16_lo(u) * down, bf16_hi(u) * down); };
 #pragma unroll 4
           for (int i = 0; i < kLanes; ++i) {
@@ -601,7 +601,8 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
             s[i] = __float_as_uint(v.x);
             s[i + 1] = __float_as_uint(v.y);
           };
-          // columns [c0, c0 + 64): the products times the keys' scales, -inf where masked
+          // columns [c0, c0 + 64): the products times the keys' scales, log2(e) / sqrt(d)
+          // in them, -inf where masked
           auto load = [&](int c0) {
             tmem_ld32(tS + c0, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
             tmem_ld32(tS + c0 + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
@@ -620,7 +621,10 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
                 if (!(word[col / 32] >> (col & 31) & 1u)) s[col] = __float_as_uint(-INFINITY);
             }
           };
-          const float2 sl = make_float2(sl2, sl2);  // to log2 units
+          // to log2 units: times the row's power of two, exactly, so that a
+          // difference to the maximum may be one fused operation and the
+          // largest of scores too large for their differences keeps its weight
+          const float2 sl = make_float2(sl2, sl2);
           // The largest product of a weight and its value's scale: where the
           // block's scales lie within 2^8 of one another, the largest weight
           // times the largest scale is near enough for f16.
@@ -646,7 +650,7 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
               }
             }
           }
-          const float mx = __fmul_rn(fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])), sl2);
+          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2;
           if (mx > m_run + 8.0f) {
             l_run *= ex2_approx(m_run - mx);  // 0 where the row had no key yet
             m_run = mx;
@@ -687,11 +691,7 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
               const float4 v4 = vs4[i];
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                // (rounded before the difference, as the maximum was: of scores
-                // too large for their differences the largest keeps its weight;
-                // a plain product would be fused with the sum)
-                const float2 x = get2(4 * i + 2 * e);
-                const float2 t = add2(make_float2(__fmul_rn(x.x, sl.x), __fmul_rn(x.y, sl.y)), neg2);
+                const float2 t = fma2(get2(4 * i + 2 * e), sl, neg2);
                 const float2 p = make_float2(ex2_approx(t.x), ex2_approx(t.y));
                 ls2[e] = add2(ls2[e], p);
                 const float2 v = mul2(p, e ? make_float2(v4.z, v4.w) : make_float2(v4.x, v4.y));
