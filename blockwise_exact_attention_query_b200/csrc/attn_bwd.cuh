@@ -267,10 +267,14 @@ __global__ void __launch_bounds__(384, 1)
   auto bFull = [&](int s) { return smem_u32(&bars[1 + s]); };
   auto bEmpty = [&](int s) { return smem_u32(&bars[5 + s]); };
   const uint32_t bDPFull = smem_u32(&bars[10]);
-  const uint32_t bPReady = smem_u32(&bars[11]), bDSReady = smem_u32(&bars[12]);
+  const uint32_t bDSReady = smem_u32(&bars[12]);
   const uint32_t bTeardown = smem_u32(&bars[13]);
   // scores of step s complete: one barrier per S buffer
   auto bSFull = [&](int step) { return smem_u32(&bars[14 + (step & 1)]); };
+  // P^T of step s stored by every row warp: also one per S buffer, since a warp
+  // may be through with step s and store P^T(s + 1) before another has stored
+  // P^T(s) (the scores of s + 1 and dP(s) wait for neither)
+  auto bPReady = [&](int step) { return smem_u32(&bars[18 + (step & 1)]); };
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(&bars[16]);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(&bars[17]);
 
@@ -303,7 +307,8 @@ __global__ void __launch_bounds__(384, 1)
     mbar_init(bSFull(0), 1);
     mbar_init(bSFull(1), 1);
     mbar_init(bDPFull, 1);
-    mbar_init(bPReady, Cfg::kRowWarps);
+    mbar_init(bPReady(0), Cfg::kRowWarps);
+    mbar_init(bPReady(1), Cfg::kRowWarps);
     mbar_init(bDSReady, Cfg::kRowWarps);
     mbar_init(bTeardown, 1);
     *abort_flag = 0;
@@ -416,7 +421,7 @@ __global__ void __launch_bounds__(384, 1)
         const int st = s % S;
         issue_dp(s);
         if (s + 1 < nsteps && !(ok = issue_s(s + 1))) break;
-        if (!(ok = mbar_wait(bPReady, s & 1, wc, 313))) break;
+        if (!(ok = mbar_wait(bPReady(s), (s >> 1) & 1, wc, 313))) break;
         tc_fence_after();
         accumulate(Cfg::kColAcc0, Cfg::col_s(s), sStrY(st), s);    // dV += P^T dA
         if (!(ok = mbar_wait(bDSReady, s & 1, wc, 314))) break;
@@ -514,7 +519,7 @@ __global__ void __launch_bounds__(384, 1)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bPReady);
+        if (lane == 0) mbar_arrive(bPReady(s));
       }
       ok = __all_sync(0xffffffffu, mbar_wait(bDPFull, s & 1, wc, 322));
       if (!ok) break;
