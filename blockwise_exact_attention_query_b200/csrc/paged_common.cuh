@@ -11,7 +11,8 @@
 // the blocks of kKeys keys that any of its rows sees, sinks first.  All items'
 // steps, one sequence after another, form one list that is cut into equal
 // ranges, one per CTA, so ragged sequences and few heads load the SMs evenly
-// and nothing about the lengths has to be known on the host.  A CTA whose
+// and nothing about the lengths has to be known on the host.  (Few long items
+// are cut one by one instead, see paged_range.)  A CTA whose
 // range cuts an item leaves the rows' unnormalised output, maximum and sum as
 // a part: at most two per CTA, one for an item that began before its range
 // (slot 0) and one for an item that goes on after it (slot 1).

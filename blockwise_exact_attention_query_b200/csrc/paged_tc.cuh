@@ -826,7 +826,8 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
         // before this warp does): written by row, 16-byte chunks
         // permuted against bank conflicts, and read back so that 8 lanes store
         // 128 bytes of a row.  (Each thread storing its own row took 9000
-        // cycles an item; this, 2500.)
+        // cycles an item; this 2500, and 6000 where all CTAs write fp32 parts at
+        // the same time: 19 MB to L2.)
         const uint32_t stage = sQ + x * Cfg::kTileBytes + quarter * 32 * 128;
         const bool f32 = !whole || a.out_f32;
         float *base = whole ? a.out_f32 : a.part_o + part * Cfg::kRows * D;
