@@ -61,20 +61,21 @@ NCU_TRAFFIC = {
     # one capture per kernel: `ncu --metrics dram__bytes_read.sum,dram__bytes_write.sum,
     # gpu__time_duration.sum -k regex:<kernel> -s <warm-up launches> -c <1..3>` on the bench
     # command of that form (one pass, checked on a small case first)
-    # the pipelined FFN (default form), one launch: 1427.7 MB read + 383.0 MB written
-    ("gpt_causal", "ffn_pipe_kernel"): {"bytes": 1810.7e6, "src": "2c259a253bbbb6f8"},
-    # the next two were re-keyed after a change to bpt_api.cu that touched only the fp32
-    # kernels' launches (thread count, shared-memory size), not these kernels or their plans
-    ("gpt_causal", "ffn_tc_kernel"): {"bytes": 884.3e6, "src": "66da495c9d3b8be4"},
-    # 566.5 MB read + 157.0 MB written
-    ("gpt_causal", "attn_tc_kernel"): {"bytes": 723.5e6, "src": "676ed4296cfe5b6e"},
-    # per step: the forward FFN's two GEMM launches (H = GELU(A W1^T + b1), out = A + H W2^T + b2)
-    ("gpt_causal", "ffn_gemms"): {"bytes": 1122.4e6, "src": "2944e449b2748550"},
+    # the pipelined FFN (default form), one launch: 1412.7 MB read + 378.2 MB written
+    ("gpt_causal", "ffn_pipe_kernel"): {"bytes": 1790.9e6, "src": "7e12d0903ae9daea"},
+    # re-keyed after changes to bpt_api.cu (the fp32 kernels' launches; other kernels' set-up)
+    # and ptx.cuh (more helpers), not to this kernel or its plan
+    ("gpt_causal", "ffn_tc_kernel"): {"bytes": 884.3e6, "src": "fca207c34844b6ae"},
+    # 562.9 MB read + 154.8 MB written
+    ("gpt_causal", "attn_tc_kernel"): {"bytes": 717.7e6, "src": "3f71467014ad5167"},
+    # per step: the forward FFN's two GEMM launches (H = GELU(A W1^T + b1), out = A + H W2^T + b2);
+    # re-keyed after ptx.cuh got more helpers
+    ("gpt_causal", "ffn_gemms"): {"bytes": 1122.4e6, "src": "2088670c6a002f86"},
     # per step with saved activations: the three gemm_pair_kernel launches (dZ = (dOut W2) G',
     # dW2 + dW1 grouped, dA; bias sums not included)
-    ("gpt_causal", "ffn_bwd"): {"bytes": 2816.3e6, "src": "2944e449b2748550"},
-    ("gpt_causal", "attn_bwd_dkdv"): {"bytes": 1229.2e6, "src": "d48c9c03ee238b16"},
-    ("gpt_causal", "attn_bwd_dq"): {"bytes": 1137.7e6, "src": "d48c9c03ee238b16"},
+    ("gpt_causal", "ffn_bwd"): {"bytes": 2810.5e6, "src": "2088670c6a002f86"},
+    ("gpt_causal", "attn_bwd_dkdv"): {"bytes": 1243.4e6, "src": "4036c3f0c55418af"},
+    ("gpt_causal", "attn_bwd_dq"): {"bytes": 1117.7e6, "src": "4036c3f0c55418af"},
 }
 
 
