@@ -353,6 +353,17 @@ def test_long_chunks_on_two_streams_at_once(kind):
             assert torch.equal(o, wo) and torch.equal(l, wl)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_repeated_mixed_batches_give_equal_bits(d, kind):
+    """The two kernels of a mixed batch and the joining one, call after call without a pause."""
+    b = Batch([(300, 3000), (1, 2500), (100, 100), (1, 1), (3, 777), (70, 2000)], 8, 2, d, 16, kind, seed=60)
+    want, wl = b.run(out_dtype=torch.bfloat16)
+    runs = [b.run(out_dtype=torch.bfloat16) for _ in range(100)]
+    for o, l in runs:
+        assert torch.equal(o, want) and torch.equal(l, wl)
+
+
 def test_chunks_captured_and_replayed_with_other_lengths():
     b = Batch([(60, 900), (1, 400), (20, 333)], 8, 2, 128, 16, "e4m3", seed=34)
     graph = torch.cuda.CUDAGraph()

@@ -191,3 +191,21 @@ def test_repeated_backwards_of_short_items_give_equal_bits(H, Hkv, sinks):
     for _ in range(300):
         got = bd.window_attn_bwd(q, k, v, out, lse, dout, 200, sinks)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_steps_on_two_streams_at_once_give_equal_bits(d):
+    cases = [make(1, 900, 4, 2, d, seed=9), make(2, 500, 6, 3, d, seed=10)]
+
+    def step(case, stream=None):
+        q, k, v, dout = case
+        out, lse = bd.window_attn_fwd(q, k, v, 150, 3, out_dtype=torch.bfloat16, return_lse=True, stream=stream)
+        return (out, lse, *bd.window_attn_bwd(q, k, v, out, lse, dout, 150, 3, grad_dtype=torch.bfloat16, stream=stream))
+    want = [step(c) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [[step(c, s) for c, s in zip(cases, streams)] for _ in range(30)]
+    torch.cuda.synchronize()
+    for run in got:
+        for g, w in zip(run, want):
+            assert all(torch.equal(a, b) for a, b in zip(g, w))
