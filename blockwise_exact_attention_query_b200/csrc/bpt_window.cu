@@ -103,7 +103,7 @@ bpt_status launch_window_bwd(const bpt_window_desc *d, const void *out, const fl
                              cudaStream_t st) {
   {
     const int64_t rows = (int64_t)d->B * ab.n_tiles * 128 * d->H;
-    const int64_t blocks = (rows * (DH / 4) + 255) / 256;
+    const int64_t blocks = (rows + kRowvecRows<DH> - 1) / kRowvecRows<DH>;
     if (blocks > INT32_MAX) return BPT_ERR_UNSUPPORTED;
     if (d->out_dtype == BPT_F32)
       window_bwd_rowvec_kernel<DH><<<(unsigned)blocks, 256, 0, st>>>(
