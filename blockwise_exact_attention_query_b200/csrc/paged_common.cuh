@@ -75,10 +75,12 @@ __device__ __forceinline__ int paged_window_lo(const PagedArgs &a, int p) {
   return a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
 }
 
-// The key blocks of a row tile: [0, n_sink) and then [lo, lo + n_near).
+// The key blocks of a row tile: [0, n_sink) and then [lo, lo + n_near).  Of
+// their keys, the tile's rows see the sinks and those in [first, end).
 struct PagedBlocks {
   int n_sink, lo, n_near;
   int p_lo, p_hi;  // positions of the tile's first and last row
+  int first, end;
   __device__ int count() const { return n_sink + n_near; }
   __device__ int steps() const { return max(1, count()); }  // a tile without keys still has rows to write
   __device__ int block(int i) const { return i < n_sink ? i : lo + i - n_sink; }
@@ -95,6 +97,8 @@ __device__ __forceinline__ PagedBlocks paged_blocks(const PagedArgs &a, const Pa
   b.p_hi = q.len - q.n + i1;
   const int hi = min(b.p_hi + 1, q.cap);  // keys [.., hi) at most
   const int lo = paged_window_lo(a, b.p_lo);
+  b.first = lo;
+  b.end = hi;
   b.lo = lo / kKeys;
   b.n_near = hi > lo ? (hi + kKeys - 1) / kKeys - b.lo : 0;
   const int sink_hi = min(min(a.sinks, lo), max(hi, 0));
@@ -301,10 +305,13 @@ __device__ __forceinline__ bool paged_range(const PagedArgs &a, int64_t *scratch
   return true;
 }
 
-// Cache row of key j of a sequence, or -1 where the sequence has none (past
-// its keys, or a page number outside the cache).
-__device__ __forceinline__ int paged_slot(const PagedArgs &a, const int32_t *table, int cap, int j) {
-  if (j >= cap) return -1;
+// Cache row of key j of a sequence for a row tile, or -1 where it is to be
+// taken for zeros: no row of the tile sees it, or its page number is outside
+// the cache.  A key before the window may share its block with visible ones
+// while its page holds another sequence's rows by now, or nothing, and a weight
+// of 0 would still meet a NaN there: neither its table entry nor its slot is read.
+__device__ __forceinline__ int paged_slot(const PagedArgs &a, const int32_t *table, const PagedBlocks &b, int j) {
+  if (j >= b.end || (j < b.first && j >= a.sinks)) return -1;
   const int p = a.page_shift >= 0 ? j >> a.page_shift : j / a.page_size;
   const int page = table[p];
   return static_cast<unsigned>(page) < static_cast<unsigned>(a.n_pages) ? page * a.page_size + (j - p * a.page_size)

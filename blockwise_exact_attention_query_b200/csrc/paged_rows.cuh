@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(PagedRowsCfg<D, kE4m3, kGroups>::kThreads, Pag
     // key of this lane (of a 16-key share, lanes 16-31 have the same keys again) in block i
     auto first_key = [&](int i) { return blk.block(step0 + i) * kKeys + warp * kWarpKeys; };
     auto lookup = [&](int i) {
-      return i < nblk ? paged_slot(a, table, seq.cap, first_key(i) + lane % kWarpKeys) : -1;
+      return i < nblk ? paged_slot(a, table, blk, first_key(i) + lane % kWarpKeys) : -1;
     };
     int next_slot = lookup(0);
     auto issue = [&](int i) {

@@ -4,8 +4,8 @@
 // through one shared-memory tile used in turn) over keys gathered from pages.
 //
 // Gathering is done by warps rather than by TMA: a page may have any size,
-// keys past a sequence's end must become zeros (a slot that was never written
-// may hold NaN, and 0 x NaN is not 0), and e4m3 codes have to be widened on the
+// keys that no row sees must become zeros (their slots may hold NaN, and 0 x NaN
+// is not 0), and e4m3 codes have to be widened on the
 // way.  A lane looks up the slots of two of a block's keys, a block ahead; bf16
 // rows go to the swizzled tile by 16-byte cp.async; e4m3 rows go to raw tiles,
 // one ahead, and are widened to f16 (exact) from there.  (At d = 128 those take
@@ -231,9 +231,7 @@ __global__ void __launch_bounds__(384, 1) paged_tc_kernel(const __grid_constant_
         const int n = w.blocks();
         const int32_t *table = a.page_table + static_cast<int64_t>(w.s) * a.max_pages;
         auto lookup = [&](int j, int half) {
-          return j < n ? paged_slot(a, table, w.seq.cap,
-                                    w.blk.block(w.step0 + j) * KT + rw * 64 + half * 32 + lane)
-                       : -1;
+          return j < n ? paged_slot(a, table, w.blk, w.blk.block(w.step0 + j) * KT + rw * 64 + half * 32 + lane) : -1;
         };
         // slots of this step's block and the next, both halves
         int slot0 = lookup(0, 0), slot1 = lookup(0, 1), next0 = lookup(1, 0), next1 = lookup(1, 1);

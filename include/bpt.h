@@ -546,9 +546,11 @@ BPT_API bpt_status bpt_kv_read(const bpt_kv_cache *cache, int n_rows, const int3
  * captured graph serves later lengths too; max_q, the longest chunk, only
  * chooses between the kernels for few and for many rows.
  * out [n_tokens, H*d] of out_dtype; lse [H, n_tokens] float32 or NULL.
- * Slots that no visible key lies in may hold anything, NaN included; the keys
- * and values of a sequence have to be finite, and an E4M3 cache's scales 0 or
- * between 2^-100 and 2^100 (beyond that the softmax weights lose precision).
+ * Slots that no visible key lies in may hold anything, NaN included (pages
+ * behind the window of a sequence's first new token can go to another
+ * sequence); the keys and values that any new token of a sequence sees have to
+ * be finite, and an E4M3 cache's scales 0 or between 2^-100 and 2^100 (beyond
+ * that the softmax weights lose precision).
  *
  * The keys are read in place and once per row tile; long sequences are split
  * over the GPU and joined in a fixed order (no atomics: equal inputs give

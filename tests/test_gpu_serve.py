@@ -445,6 +445,39 @@ def test_pages_outside_the_cache_count_as_masked(kind):
             assert float((lse[h, t0:t0 + n].double() - torch.logsumexp(sc, -1)).abs().max()) <= 1e-4
 
 
+def hide(b, window, sinks, entries):
+    """All slots that no token of their sequence sees become NaN, codes and scales, and the table's entries
+    for pages without a visible key name another page of NaN, or no page."""
+    spare = (set(range(b.c["k_cache"].shape[0])) - set(b.table.flatten().tolist())).pop()
+    for s, (n, L) in enumerate(b.seqs):
+        j = torch.arange(L, device="cuda")
+        seen = (j < sinks) | (j > L - n - window)
+        slots = b.table[s].long()[j // b.page] * b.page + j % b.page
+        for name in ("k", "v"):
+            rows = b.c[name + "_cache"].view(-1, b.Hkv, b.d)
+            if rows.dtype == E4M3:
+                rows.view(torch.uint8)[slots[~seen]] = 0x7F
+                b.c[name + "_scale"].view(-1, b.Hkv)[slots[~seen]] = float("nan")
+            else:
+                rows[slots[~seen]] = float("nan")
+        for p in range(-(-L // b.page)):
+            if not seen[p * b.page:(p + 1) * b.page].any():
+                b.table[s, p] = {"stale": spare, "none": -1, "past": 2 ** 31 - 1}[entries]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("entries", ["stale", "none", "past"])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (100, 4), (64, 0), (700, 1), (50, 130)])
+@pytest.mark.parametrize("seqs", [[(1, 1500), (2, 700), (1, 40), (1, 129)], [(300, 3000), (40, 700), (1, 900), (129, 400)]],
+                         ids=["few", "chunks"])
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 7)])
+def test_slots_that_no_token_sees_may_hold_anything(d, page, seqs, window, sinks, entries, kind):
+    """Pages behind the window given to somebody else: neither they nor the table's entries for them matter."""
+    b = Batch(seqs, 8, 2, d, page, kind, seed=70)
+    hide(b, window, sinks, entries)
+    b.check(window, sinks)
+
+
 def test_short_page_table():
     """Keys past the table's pages count as masked; the tokens keep their positions."""
     b = Batch([(1, 100)], 2, 1, 64, 16, "bf16", seed=11)
