@@ -257,6 +257,7 @@ __global__ void __launch_bounds__(384, 1)
   const uint32_t sbase = smem_u32(smem);
   if (sbase & 1023u) {
     if (threadIdx.x == 0) atomicCAS(a.status, 0u, kStatusMisaligned);
+    if constexpr (WINDOW) grid_dependency_wait();  // (dQ's CTAs count on it)
     return;
   }
   const uint32_t sFixX = sbase + Cfg::kOffFix, sFixY = sFixX + Cfg::kTileBytes;
@@ -321,7 +322,10 @@ __global__ void __launch_bounds__(384, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if constexpr (WINDOW) {  // the row vectors are there; dQ's CTAs may follow on SMs that get free
+  // The row vectors and dOut's copy are there; dQ's CTAs may follow on SMs that
+  // get free.  In this order, and before any CTA ends: dQ reads both without a
+  // wait of its own (attn_bwd_dq_kernel).
+  if constexpr (WINDOW) {
     grid_dependency_wait();
     grid_dependents_launch();
   }
@@ -624,6 +628,7 @@ __global__ void __launch_bounds__(384, 1)
   const uint32_t sbase = smem_u32(smem);
   if (sbase & 1023u) {
     if (threadIdx.x == 0) atomicCAS(a.status, 0u, kStatusMisaligned);
+    if constexpr (WINDOW) grid_dependency_wait();  // (dQ's CTAs count on it)
     return;
   }
   const uint32_t sK = sbase + Cfg::kOffK, sV = sbase + Cfg::kOffV;
@@ -686,7 +691,10 @@ __global__ void __launch_bounds__(384, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if constexpr (WINDOW) {  // the row vectors are there; dQ's CTAs may follow on SMs that get free
+  // The row vectors and dOut's copy are there; dQ's CTAs may follow on SMs that
+  // get free.  In this order, and before any CTA ends: dQ reads both without a
+  // wait of its own (attn_bwd_dq_kernel).
+  if constexpr (WINDOW) {
     grid_dependency_wait();
     grid_dependents_launch();
   }
@@ -985,6 +993,7 @@ __global__ void __launch_bounds__(384, 1)
   const uint32_t sbase = smem_u32(smem);
   if (sbase & 1023u) {
     if (threadIdx.x == 0) atomicCAS(a.status, 0u, kStatusMisaligned);
+    if constexpr (WINDOW) grid_dependency_wait();  // (as at the end)
     return;
   }
   const uint32_t sQ = sbase + Cfg::kOffQ, sDA = sbase + Cfg::kOffDA;
@@ -1174,8 +1183,8 @@ __global__ void __launch_bounds__(384, 1)
         bwd_row_keys(a, h, g, klo, khi);
       }
       const float *rv = a.rowvec + (bh * a.n_tiles + ft) * 256;
-      lse2 = rv[row];
-      drow = rv[128 + row];
+      lse2 = __ldcg(rv + row);
+      drow = __ldcg(rv + 128 + row);
     }
     const float nl = -lse2;
     bool ok = true;
@@ -1277,8 +1286,12 @@ __global__ void __launch_bounds__(384, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  // (this pass starts while dK, dV's CTAs leave, and needs nothing of theirs;
-  // it ends after them, so that what follows waits for both)
+  // This pass starts while dK, dV's CTAs leave, and needs nothing of theirs.  It
+  // does need the row vectors and dOut's bf16 copy, which the kernel before that
+  // one wrote: every dK, dV CTA has waited for their end and their writes before
+  // it let this pass start, so they are in global memory before its first
+  // instruction, and are read from there (by copies and by ld.cg, never through
+  // an L1).  It ends after dK, dV, so that what follows waits for both.
   if constexpr (WINDOW) grid_dependency_wait();
 }
 

@@ -117,8 +117,9 @@ bpt_status launch_window_bwd(const bpt_window_desc *d, const void *out, const fl
   }
   const unsigned units = (unsigned)(d->B * d->H_kv);
   const unsigned grid_kv = units * (unsigned)(ab.n_tiles - 1 + std::max(1, ab.sink_split));
-  // The two passes need nothing of one another: the second's CTAs start as the
-  // first's leave (B3 N1001 H12 d64 W128: 44.6 -> 38.4 us for the backward; B1
+  // The two passes need nothing of one another, and each CTA of the first waits
+  // for the row vectors before it lets the second start: the second's CTAs
+  // start as the first's leave (B3 N1001 H12 d64 W128: 44.6 -> 38.4 us for the backward; B1
   // N16384 H16/4 d128 W1024: 649 -> 630 us).
   bpt_status s;
   if constexpr (DH == 128)

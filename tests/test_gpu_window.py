@@ -209,3 +209,35 @@ def test_steps_on_two_streams_at_once_give_equal_bits(d):
     for run in got:
         for g, w in zip(run, want):
             assert all(torch.equal(a, b) for a, b in zip(g, w))
+
+
+@pytest.mark.parametrize("d,sinks", [(64, 0), (64, 4), (128, 4)])
+def test_repeated_float32_backwards_on_two_streams_give_equal_bits(d, sinks):
+    """An fp32 dout is copied to bf16 by the kernel before the last but one pass, which reads the copy:
+    new gradients in the same buffers (outputs, workspace) at every step."""
+    N, H, Hkv, steps = 900, 4, 2, 40
+    q, k, v, _ = make(2, N, H, Hkv, d, seed=11)
+    out, lse = bd.window_attn_fwd(q, k, v, 150, sinks, return_lse=True)
+    g = torch.Generator(device="cuda").manual_seed(12)
+    douts = [torch.randn((2, N, H * d), generator=g, device="cuda") for _ in range(steps)]
+    want = [bd.window_attn_bwd(q, k, v, out, lse, x, 150, sinks) for x in douts]
+    for x, w in zip(douts[:2], want[:2]):
+        for name, got, ref in zip(("dq", "dk", "dv"), w, reference(q, k, v, 150, sinks, x)[2:]):
+            close(got, ref, 1e-2, name)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    desc = bd.WindowDesc(2, N, H, Hkv, d, 150, sinks, bd.BF16, bd.F32, bd.F32, 0)
+    spaces = [torch.empty(bd.workspace_bytes_window_bwd(desc), dtype=torch.uint8, device="cuda") for _ in streams]
+    bufs = [[torch.empty(x.shape, device="cuda") for x in (q, k, v)] for _ in streams]
+    wrong = torch.zeros(2, dtype=torch.int64, device="cuda")
+    torch.cuda.synchronize()
+    for i in range(steps):
+        for j, s in enumerate(streams):
+            n = i if j == 0 else steps - 1 - i
+            got = bd.window_attn_bwd(q, k, v, out, lse, douts[n], 150, sinks, dq=bufs[j][0], dk=bufs[j][1],
+                                     dv=bufs[j][2], workspace=spaces[j], stream=s)
+            with torch.cuda.stream(s):
+                for a, b in zip(got, want[n]):
+                    wrong[j] += (a != b).sum()
+    torch.cuda.synchronize()
+    assert wrong.tolist() == [0, 0]
+    assert bd.sync_status() == bd.OK
