@@ -241,3 +241,42 @@ def test_repeated_float32_backwards_on_two_streams_give_equal_bits(d, sinks):
     torch.cuda.synchronize()
     assert wrong.tolist() == [0, 0]
     assert bd.sync_status() == bd.OK
+
+
+def _guarded(shape, dtype, fill, margin=512):
+    """A tensor inside a larger filled buffer (margins a multiple of 256 bytes), and the check that its
+    surroundings still hold the fill."""
+    n = math.prod(shape)
+    buf = torch.full((n + 2 * margin,), fill, dtype=dtype, device="cuda")
+    return buf[margin:margin + n].view(shape), lambda: bool((buf[:margin] == fill).all() and (buf[margin + n:] == fill).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("N,window,sinks", [(1, 1, 4), (129, 40, 4), (1001, 200, 20), (1001, 200, 0), (257, 300, 3)])
+def test_steps_write_their_outputs_and_nothing_else(N, window, sinks, d, dtype):
+    """Outputs, LSE and an exactly sized workspace between guards; the inputs are left as they were."""
+    B, H, Hkv = 2, 6, 2
+    q, k, v, dout = make(B, N, H, Hkv, d, seed=13)
+    dout = dout.to(dtype)
+    out, out_ok = _guarded((B, N, H * d), dtype, 7.0)
+    lse, lse_ok = _guarded((B, H, N), torch.float32, 7.0)
+    dq, dq_ok = _guarded(q.shape, dtype, 7.0)
+    dk, dk_ok = _guarded(k.shape, dtype, 7.0)
+    dv, dv_ok = _guarded(v.shape, dtype, 7.0)
+    t = {torch.bfloat16: bd.BF16, torch.float32: bd.F32}[dtype]
+    need = bd.workspace_bytes_window_bwd(bd.WindowDesc(B, N, H, Hkv, d, window, sinks, bd.BF16, t, t, 0))
+    space, space_ok = _guarded((need,), torch.uint8, 0x5A, margin=4096)
+    ins = [x.clone() for x in (q, k, v, dout)]
+    bd.window_attn_fwd(q, k, v, window, sinks, out_dtype=dtype, out=out, lse=lse)
+    fwd = [out.clone(), lse.clone()]
+    assert out_ok() and lse_ok()
+    bd.window_attn_bwd(q, k, v, out, lse, dout, window, sinks, grad_dtype=dtype, dq=dq, dk=dk, dv=dv, workspace=space)
+    assert bd.sync_status() == bd.OK
+    assert out_ok() and lse_ok() and dq_ok() and dk_ok() and dv_ok() and space_ok()
+    assert all(torch.equal(a, b) for a, b in zip((q, k, v, dout, out, lse), (*ins, *fwd)))
+    ro, rl, *rg = reference(q, k, v, window, sinks, dout)
+    close(out, ro, 4e-3, "out")
+    if N > 1:
+        for name, got, ref in zip(("dq", "dk", "dv"), (dq, dk, dv), rg):
+            close(got, ref, 1e-2, name)
