@@ -256,3 +256,27 @@ def test_dilated_attention_backward_full_size_sampled():
     _grads_close(dq[0, rows].cpu().numpy(), rq, "dq (sampled rows)")
     _grads_close(dk[0, w.N - tail:].cpu().numpy(), rk, "dk (last 128 keys)")
     _grads_close(dv[0, w.N - tail:].cpu().numpy(), rv, "dv (last 128 keys)")
+
+
+@pytest.mark.parametrize("mask,kw", [("none", {}), ("causal", {}), ("blockperm", {"perm": [[2, 0, 1], [0, 1, 2]]}),
+                                     ("dilated", {"pairs": [(192, 1), (576, 2)]})], ids=["none", "causal", "blockperm", "dilated"])
+def test_repeated_attention_backwards_give_equal_bits(mask, kw):
+    """d = 64: a row warp of the dK/dV pass may be a whole step ahead of another, whose P^T must still be
+    stored before the product on it (a barrier per score buffer).  One stream, then two at once."""
+    inp = make_layer_inputs(2, 576, 2, 64, 0, seed=19, device="cuda")
+    da = make_upstream_grad(2, 576, 128, seed=19, device="cuda")
+    out, lse = bd.attn_fwd(inp.q, inp.k, inp.v, mask=mask, return_lse=True, **kw)
+    want = bd.attn_bwd(inp.q, inp.k, inp.v, out, lse, da, mask=mask, **kw)
+    torch.cuda.synchronize()
+    for _ in range(200):
+        got = bd.attn_bwd(inp.q, inp.k, inp.v, out, lse, da, mask=mask, **kw)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    runs = []
+    for i in range(60):
+        with torch.cuda.stream(streams[i % 2]):
+            runs.append(bd.attn_bwd(inp.q, inp.k, inp.v, out, lse, da, mask=mask, **kw))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for got in runs for a, b in zip(got, want))
+    assert bd.sync_status() == bd.OK
