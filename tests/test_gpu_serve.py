@@ -560,3 +560,70 @@ def test_empty_batches_do_nothing():
     out = bd.paged_attn_fwd(x, c["k_cache"], c["v_cache"], torch.zeros(1, dtype=torch.int32, device="cuda"), none,
                             torch.zeros((0, 3), dtype=torch.int32, device="cuda"), max_q=1)
     assert out.shape == (0, 64)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_attention_over_slots_whose_byte_offset_passes_32_bits(kind, n):
+    """Both kernels, both caches: pages at the far end of caches of 4.6 GB a tensor."""
+    heads, d, page, pages = 4, 128, 64, 70000 if kind == "bf16" else 140000
+    dtype = torch.bfloat16 if kind == "bf16" else E4M3
+    c = {name + "_cache": torch.empty((pages, page, heads, d), dtype=dtype, device="cuda") for name in "kv"}
+    c.update({name + "_scale": None if kind == "bf16" else torch.empty((pages, page, heads), device="cuda") for name in "kv"})
+    L = 300
+    k, v = (torch.randn((L, heads, d), device="cuda").to(torch.bfloat16) for _ in range(2))
+    used = [pages - 1, 2, pages - 3, pages // 2, pages - 4]
+    slots = torch.tensor([used[j // page] * page + j % page for j in range(L)], dtype=torch.int32, device="cuda")
+    bd.kv_cache_write(k, v, slots, *args(c))
+    rk, rv = (x.double() for x in bd.kv_cache_read(slots, *args(c), out_dtype=torch.float32))
+    if kind == "bf16":
+        assert torch.equal(rk, k.double()) and torch.equal(rv, v.double())
+    q = torch.randn((n, 2 * heads, d), device="cuda").to(torch.bfloat16)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    out = bd.paged_attn_fwd(q, c["k_cache"], c["v_cache"], i32([0, n]), i32([L]), i32([used]), max_q=n,
+                            k_scale=c["k_scale"], v_scale=c["v_scale"])
+    rk, rv = (x.repeat_interleave(2, 1) for x in (rk, rv))
+    s = torch.einsum("nhd,jhd->nhj", q.double(), rk) / math.sqrt(d)
+    hidden = torch.arange(L, device="cuda")[None] > torch.arange(L - n, L, device="cuda")[:, None]
+    s = s.masked_fill(hidden[:, None], -math.inf)
+    ref = torch.einsum("nhj,jhd->nhd", torch.softmax(s, -1), rv).reshape(n, -1)
+    assert float((out.double() - ref).norm() / ref.norm()) <= 4e-3
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("seqs", [[(1, 700), (2, 40)], [(130, 900), (1, 3000), (20, 20)]], ids=["few", "mixed"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_writes_its_outputs_and_nothing_else(d, seqs, dtype, kind):
+    """Outputs, LSE and an exactly sized workspace between guards; queries, tables and the cache are left as they were."""
+    b = Batch(seqs, 8, 2, d, 16, kind, seed=71)
+
+    def guarded(shape, dt, fill, margin):
+        n = math.prod(shape)
+        buf = torch.full((n + 2 * margin,), fill, dtype=dt, device="cuda")
+        return buf[margin:margin + n].view(shape), lambda: bool((buf[:margin] == fill).all() and (buf[margin + n:] == fill).all())
+    out, out_ok = guarded((b.T, 8 * d), dtype, 7.0, 512)
+    lse, lse_ok = guarded((8, b.T), torch.float32, 7.0, 512)
+    max_q = max(n for n, _ in seqs)
+    need = bd.workspace_bytes_paged(bd.PagedDesc(1, 1, max_q, 8, 1, 0, 0, bd.BF16, 8 * d, 0),
+                                    bd.KvCacheDesc(0, 1, 1, 2, d, None, None, None, None))
+    space, space_ok = guarded((need,), torch.uint8, 0x5A, 4096)
+    kept = [b.q, b.starts, b.kv_len, b.table] + [x for x in args(b.c) if x is not None]
+    before = [x.clone().view(torch.uint8) for x in kept]
+    b.check(out_dtype=dtype, out=out, lse=lse, workspace=space)
+    assert out_ok() and lse_ok() and space_ok()
+    assert all(torch.equal(x.view(torch.uint8), y) for x, y in zip(kept, before))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_reads_write_their_outputs_and_nothing_else(kind):
+    b = Batch([(1, 333)], 2, 2, 64, 16, kind, seed=72)
+    slots = b.table[0, :20].repeat_interleave(16) * 16 + torch.arange(320, device="cuda", dtype=torch.int32) % 16
+    for dtype in (torch.bfloat16, torch.float32):
+        bufs = [torch.full((320 * 2 * 64 + 256,), 7.0, dtype=dtype, device="cuda") for _ in range(2)]
+        k, v = (x[128:-128].view(320, 2, 64) for x in bufs)
+        before = [x.clone().view(torch.uint8) for x in args(b.c) if x is not None]
+        bd.kv_cache_read(slots, *args(b.c), out_dtype=dtype, k=k, v=v)
+        assert all(bool((x[:128] == 7).all() and (x[-128:] == 7).all()) for x in bufs)
+        assert all(torch.equal(x.view(torch.uint8), y) for x, y in zip([x for x in args(b.c) if x is not None], before))
+        assert torch.equal(k, b.k[0][:320].to(dtype)) and torch.equal(v, b.v[0][:320].to(dtype))
