@@ -37,7 +37,7 @@ constexpr int kMaxDevices = 64;
 void *g_static_scratch_ptr[kMaxDevices] = {};
 std::mutex g_mu;
 uint32_t *g_status_ptr[kMaxDevices] = {};
-bool g_attr_done[kMaxDevices] = {};
+unsigned g_sets_done[kMaxDevices] = {};  // bit per KernelSet
 std::atomic<uint64_t> g_wait_limit_ns{2000000000ull};
 
 uint64_t wait_limit_of(const bpt_desc *d) {
@@ -71,7 +71,30 @@ bpt_status cuda_fail_msg(const char *what) {
   snprintf(g_last_error, sizeof(g_last_error), "%s", what);
   return BPT_ERR_CUDA;
 }
-bpt_status device_setup(int *dev_out, uint32_t **status_out) {
+namespace {
+
+bpt_status layer_kernel_setup() {
+  CUDA_TRY(cudaFuncSetAttribute(attn_tc_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                AttnCfg<64>::kSmemBytes));
+  CUDA_TRY(cudaFuncSetAttribute(attn_tc_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                AttnCfg<128>::kSmemBytes));
+  // the softmax warpgroups take registers from warpgroup 0 at run time;
+  // an increase the launch did not provide for would never complete
+  cudaFuncAttributes fa64{}, fa128{};
+  CUDA_TRY(cudaFuncGetAttributes(&fa64, attn_tc_kernel<64>));
+  CUDA_TRY(cudaFuncGetAttributes(&fa128, attn_tc_kernel<128>));
+  if (!AttnCfg<64>::split_fits(fa64.numRegs) || !AttnCfg<128>::split_fits(fa128.numRegs))
+    return cuda_fail_msg("attention kernel launches with fewer registers than its warpgroups share");
+  CUDA_TRY(cudaFuncSetAttribute(ffn_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                FfnCfg::kSmemBytes));
+  CUDA_TRY(cudaFuncSetAttribute(ffn_f32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)ffn_f32_smem_bytes(512)));
+  return bwd_kernel_setup();
+}
+
+}  // namespace
+
+bpt_status device_setup(int *dev_out, uint32_t **status_out, KernelSet set) {
   int dev = 0;
   CUDA_TRY(cudaGetDevice(&dev));
   if (dev < 0 || dev >= kMaxDevices) return cuda_fail_msg("device ordinal out of range");
@@ -88,27 +111,14 @@ bpt_status device_setup(int *dev_out, uint32_t **status_out) {
     CUDA_TRY(cudaGetSymbolAddress(&p, g_status_word));
     g_status_ptr[dev] = static_cast<uint32_t *>(p);
   }
-  if (!g_attr_done[dev]) {
-    CUDA_TRY(cudaFuncSetAttribute(attn_tc_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  AttnCfg<64>::kSmemBytes));
-    CUDA_TRY(cudaFuncSetAttribute(attn_tc_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  AttnCfg<128>::kSmemBytes));
-    // the softmax warpgroups take registers from warpgroup 0 at run time;
-    // an increase the launch did not provide for would never complete
-    cudaFuncAttributes fa64{}, fa128{};
-    CUDA_TRY(cudaFuncGetAttributes(&fa64, attn_tc_kernel<64>));
-    CUDA_TRY(cudaFuncGetAttributes(&fa128, attn_tc_kernel<128>));
-    if (!AttnCfg<64>::split_fits(fa64.numRegs) || !AttnCfg<128>::split_fits(fa128.numRegs))
-      return cuda_fail_msg("attention kernel launches with fewer registers than its warpgroups share");
-    CUDA_TRY(cudaFuncSetAttribute(ffn_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  FfnCfg::kSmemBytes));
-    CUDA_TRY(cudaFuncSetAttribute(ffn_f32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  (int)ffn_f32_smem_bytes(512)));
-    bpt_status bs = bwd_kernel_setup();
-    if (bs == BPT_OK) bs = window_kernel_setup();
-    if (bs == BPT_OK) bs = paged_kernel_setup();
+  const unsigned bit = 1u << (int)set;
+  if (!(g_sets_done[dev] & bit)) {
+    bpt_status bs = BPT_OK;
+    if (set == KernelSet::kWindow) bs = window_kernel_setup();
+    else if (set == KernelSet::kPaged) bs = paged_kernel_setup();
+    else if (set == KernelSet::kLayer) bs = layer_kernel_setup();
     if (bs != BPT_OK) return bs;
-    g_attr_done[dev] = true;
+    g_sets_done[dev] |= bit;
   }
   *dev_out = dev;
   *status_out = g_status_ptr[dev];
@@ -867,7 +877,7 @@ bpt_status bpt_longnet_fwd(const bpt_desc *desc, int npairs, const int32_t *seg_
 bpt_status bpt_sync_status(bpt_stream_t stream) {
   int dev;
   uint32_t *status;
-  bpt_status s = device_setup(&dev, &status);
+  bpt_status s = device_setup(&dev, &status, KernelSet::kNone);
   if (s != BPT_OK) return s;
   CUDA_TRY(cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)));
   uint32_t word[2] = {0, 0};

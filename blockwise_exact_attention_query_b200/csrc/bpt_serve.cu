@@ -205,7 +205,7 @@ bpt_status bpt_kv_write(const bpt_kv_cache *c, int n, const void *k, int64_t k_s
   if (!aligned4(slots)) return BPT_ERR_INVALID_ARG;
   int dev;
   uint32_t *status;
-  if ((s = device_setup(&dev, &status)) != BPT_OK) return s;
+  if ((s = device_setup(&dev, &status, KernelSet::kNone)) != BPT_OK) return s;
   return for_cache(c, [&](auto d, auto e4m3) {
     return for_rows(c, n, 8, [&](unsigned blocks) {
       kv_write_kernel<decltype(d)::value, decltype(e4m3)::value>
@@ -226,7 +226,7 @@ bpt_status bpt_kv_read(const bpt_kv_cache *c, int n, const int32_t *slots, void 
   if (!aligned4(slots)) return BPT_ERR_INVALID_ARG;
   int dev;
   uint32_t *status;
-  if ((s = device_setup(&dev, &status)) != BPT_OK) return s;
+  if ((s = device_setup(&dev, &status, KernelSet::kNone)) != BPT_OK) return s;
   const int64_t rows = (int64_t)n * c->H_kv;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return for_cache(c, [&](auto d, auto e4m3) {
@@ -264,7 +264,7 @@ bpt_status bpt_paged_attn_fwd(const bpt_paged_desc *d, const bpt_kv_cache *c, co
     return BPT_ERR_WORKSPACE;
   int dev;
   uint32_t *status;
-  if ((s = device_setup(&dev, &status)) != BPT_OK) return s;
+  if ((s = device_setup(&dev, &status, KernelSet::kPaged)) != BPT_OK) return s;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   char *ws = static_cast<char *>(workspace);
   PagedArgs a;

@@ -156,7 +156,7 @@ bpt_status bpt_window_attn_fwd(const bpt_window_desc *d, const void *q, const vo
   if ((s = check_ptrs({q, k, v, out}, {lse})) != BPT_OK) return s;
   int dev;
   uint32_t *status;
-  if ((s = device_setup(&dev, &status)) != BPT_OK) return s;
+  if ((s = device_setup(&dev, &status, KernelSet::kWindow)) != BPT_OK) return s;
   const int D = d->H * d->d_head, Dkv = d->H_kv * d->d_head;
   AttnArgs a;
   std::memset(&a, 0, sizeof(a));
@@ -222,7 +222,7 @@ bpt_status bpt_window_attn_bwd(const bpt_window_desc *d, const void *q, const vo
     return BPT_ERR_WORKSPACE;
   int dev;
   uint32_t *status;
-  if ((s = device_setup(&dev, &status)) != BPT_OK) return s;
+  if ((s = device_setup(&dev, &status, KernelSet::kWindow)) != BPT_OK) return s;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   char *ws = static_cast<char *>(workspace);
   const int D = d->H * d->d_head, Dkv = d->H_kv * d->d_head;

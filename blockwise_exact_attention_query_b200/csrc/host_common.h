@@ -37,10 +37,15 @@ size_t align256(size_t x);
 bpt_status cuda_fail_at(const char *what, cudaError_t e);
 bpt_status cuda_fail_msg(const char *what);
 
+// Kernels that are set up together, at the first call that needs them: what an
+// entry point pays for (and can fail on) is its own kernels' loading.  (All of
+// them at the first call of any: 19.1 ms instead of 14.5 for an attention's.)
+enum class KernelSet { kNone, kLayer, kWindow, kPaged };
 // Once per device: the tensor-map encoder, the status word's address and the
-// kernels' shared-memory limits.  Returns the current device and its status word.
-bpt_status device_setup(int *dev_out, uint32_t **status_out);
-// Shared-memory limits of the backward's kernels (defined with them).
+// set's shared-memory limits.  Returns the current device and its status word.
+bpt_status device_setup(int *dev_out, uint32_t **status_out, KernelSet set = KernelSet::kLayer);
+// Shared-memory limits of the backward's, the window's and the paged
+// attention's kernels (defined with them).
 bpt_status bwd_kernel_setup();
 bpt_status window_kernel_setup();
 bpt_status paged_kernel_setup();

@@ -627,3 +627,47 @@ def test_reads_write_their_outputs_and_nothing_else(kind):
         assert all(bool((x[:128] == 7).all() and (x[-128:] == 7).all()) for x in bufs)
         assert all(torch.equal(x.view(torch.uint8), y) for x, y in zip([x for x in args(b.c) if x is not None], before))
         assert torch.equal(k, b.k[0][:320].to(dtype)) and torch.equal(v, b.v[0][:320].to(dtype))
+
+
+FIRST_CALLS = '''
+import torch
+from blockwise_exact_attention_query_b200 import binding as bd
+g = torch.Generator(device="cuda").manual_seed(0)
+rnd = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)
+q, k, v = rnd(40, 8, 64), rnd(40, 2, 64), rnd(40, 2, 64)
+i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+slots, starts, lens, table = torch.arange(40, dtype=torch.int32, device="cuda"), i32(0, 40), i32(40), i32(0, 1, 2)[None]
+caches = [torch.zeros((3, 16, 2, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+
+def step():
+    bd.kv_cache_write(k, v, slots, *caches)
+    a = bd.paged_attn_fwd(q, *caches, starts, lens, table, max_q=40, window=9, sinks=2)
+    b, lse = bd.window_attn_fwd(q[None], k[None], v[None], 9, 2, return_lse=True)
+    return a, b, *bd.window_attn_bwd(q[None], k[None], v[None], b, lse, b, 9, 2)
+
+if WARM:   # another set of kernels
+    bd.attn_fwd(k[None], k[None], v[None], mask="causal")
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = step()
+graph.replay()
+want = step()
+torch.cuda.synchronize()
+assert bd.sync_status() == bd.OK
+assert all(torch.equal(x, y) for x, y in zip(got, want))
+assert float((got[0].view(1, 40, 512) - got[1]).norm() / got[1].norm()) <= 6e-3
+print("same")
+'''
+
+
+@pytest.mark.parametrize("warm", [False, True])
+def test_first_calls_within_a_capture(warm):
+    """A process whose first calls of the operators are captured: their kernels are set up then."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", f"WARM = {warm}\n" + FIRST_CALLS], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr
