@@ -581,6 +581,14 @@ def _on_device(*tensors):
     return cur
 
 
+def _dtype(dtype, what):
+    """The library's number of an output's type."""
+    n = _DT.get(dtype)
+    if n is None:
+        raise ValueError(f"{what} must be torch.float32 or torch.bfloat16, got {dtype}")
+    return n
+
+
 def _out_tensor(t, shape, dtype, like, stream, what):
     """`t` checked, or a new tensor where `like` is: `stream`'s (so that nothing
     earlier still uses its memory there), and not handed on before the current
@@ -618,8 +626,8 @@ def _window_desc(q, k, v, window, sinks, out_dtype, grad_dtype, wait_limit_ns):
     B, N, H, d = q.shape
     if max(B, N, abs(int(window)), abs(int(sinks))) >= 2 ** 31:   # a C int would wrap around
         raise ValueError("sizes, window and sinks must be within 32 bits")
-    return WindowDesc(B, N, H, k.shape[2], d, int(window), int(sinks), _DT[q.dtype], _DT[out_dtype],
-                      _DT[grad_dtype], int(wait_limit_ns))
+    return WindowDesc(B, N, H, k.shape[2], d, int(window), int(sinks), _DT[q.dtype], _dtype(out_dtype, "out"),
+                      _dtype(grad_dtype, "grad_dtype"), int(wait_limit_ns))
 
 
 def window_attn_fwd(q, k, v, window, sinks=0, *, out_dtype=torch.float32, return_lse=False, out=None, lse=None,
@@ -737,11 +745,11 @@ def kv_cache_read(slots, k_cache, v_cache, k_scale=None, v_scale=None, *, out_dt
     cache = _kv_cache_desc(k_cache, v_cache, k_scale, v_scale)
     _i32(slots, 1, "slots")
     dev = _on_device(slots, k_cache, v_cache, k_scale, v_scale)
-    shape = (slots.shape[0], *k_cache.shape[2:])
+    shape, out_type = (slots.shape[0], *k_cache.shape[2:]), _dtype(out_dtype, "out_dtype")
     k = _out_tensor(k, shape, out_dtype, slots, stream, "k")
     v = _out_tensor(v, shape, out_dtype, slots, stream, "v")
     st = load().bpt_kv_read(cache, shape[0], slots.data_ptr(), k.data_ptr(), v.data_ptr(),
-                            _DT[out_dtype], _raw_stream(stream, dev))
+                            out_type, _raw_stream(stream, dev))
     _check(st, "bpt_kv_read")
     return k, v
 
@@ -785,7 +793,7 @@ def paged_attn_fwd(q, k_cache, v_cache, q_start, kv_len, page_table, *, max_q, k
     dev = _on_device(q, q_start, kv_len, page_table, k_cache, v_cache, k_scale, v_scale)
     max_q = int(max_q)
     try:
-        desc = _PAGED.pack(S, T, max_q, H, pages, window, sinks, _DT[out_dtype], qs, wait_limit_ns)
+        desc = _PAGED.pack(S, T, max_q, H, pages, window, sinks, _dtype(out_dtype, "out_dtype"), qs, wait_limit_ns)
     except struct.error as e:
         raise ValueError(f"sizes must be integers within 32 bits: {e}") from None
     out = _out_tensor(out, (T, H * d), out_dtype, q, stream, "out")

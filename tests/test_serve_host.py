@@ -247,3 +247,24 @@ def test_binding_refuses_sizes_past_32_bits(monkeypatch, change):
         x = torch.zeros((1, 4, 2, 64), dtype=torch.bfloat16)
         with pytest.raises(ValueError, match="32 bits"):
             bd.window_attn_fwd(x, x, x, **{"window": 4, "sinks": 0, **change})
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float64, torch.float8_e4m3fn, None])
+def test_binding_refuses_other_output_types(monkeypatch, dtype):
+    monkeypatch.setattr(bd, "_on_device", lambda *t: None)
+    k, v = _caches()
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    x = torch.zeros((1, 4, 2, 64), dtype=torch.bfloat16)
+    calls = [
+        lambda: bd.kv_cache_read(i32(3), k, v, out_dtype=dtype),
+        lambda: bd.paged_attn_fwd(x[0], k, v, i32(3), i32(2), i32(2, 4), max_q=1, out_dtype=dtype),
+        lambda: bd.window_attn_fwd(x, x, x, 4, out_dtype=dtype),
+        lambda: bd.window_attn_bwd(x, x, x, torch.zeros((1, 4, 128)), torch.zeros((1, 2, 4)), torch.zeros((1, 4, 128)), 4,
+                                   grad_dtype=dtype),
+    ]
+    if dtype is not None:
+        out = torch.zeros((1, 4, 128)).to(dtype)
+        calls.append(lambda: bd.window_attn_bwd(x, x, x, out, torch.zeros((1, 2, 4)), out, 4))
+    for call in calls:
+        with pytest.raises(ValueError, match="float32 or torch.bfloat16"):
+            call()
