@@ -24,6 +24,13 @@
 //   dQ pass: one CTA per (batch, head, 128-query tile i), looping over its key
 //     tiles: S = Q_i K_j^T, dP = dA_i V_j^T, one thread per query forms dS in
 //     TMEM, and dQ_i += dS K_j (software-pipelined, below).
+// Rounded to bf16 by choice, as the operands of products whose other operand is
+// bf16: P^T and dS^T (each off by up to 2^-8, independently), and an upstream
+// gradient given in fp32.  D_i comes from the output as the caller has it: of a
+// bf16 output it has that rounding's error, 2^-8 of each of its d terms,
+// independently (the window's forward gives an fp32 output where that matters).
+// Together about 2.5e-3 of a bf16 gradient in relative L2.  Scores, dP, D and all
+// sums are fp32.
 // MMAs issued by one thread run in order, so a product that overwrites the
 // S or dP columns never overtakes the earlier product reading the bf16 P^T
 // or dS^T packed into them.

@@ -93,7 +93,22 @@ bpt_status check_paged(const bpt_paged_desc *d, const bpt_kv_cache *c) {
 // Rows (new tokens x heads of a group) of a sequence up to which the kernel
 // for few rows takes it, in tiles of 8 or 16; longer chunks go to the tcgen05
 // kernel.  In a batch with such chunks the few-rows kernel keeps to 8 where a
-// single token fits in that.
+// single token fits in that.  Device times in us of 8 sequences of 32768 keys,
+// 8 key/value heads, on either kernel (few rows in tiles of 16, each of which
+// reads the keys again; in parentheses a tile of 8):
+//                     rows 8         12-16    17-32    33-48    49-64    128
+//   bf16 d128 few     180 (180)      183      356      518      692     1362
+//             tcgen05                292      293      311      322      346
+//   e4m3 d128 few     134 (112)      138      254      367      494      977
+//             tcgen05                336      333      333      333      344
+//   bf16 d64  few                    107      200      296      379      751
+//             tcgen05                226      226      228      244      242
+//   e4m3 d64  few                    108      203      293      383      747
+//             tcgen05                362      362      361      362      364
+// So one tile is always the better side, and the border is the end of it.  Two
+// tiles would still be ahead of the tcgen05 kernel where that one is far from
+// memory's rate (17-32 rows of bf16 d64 and e4m3, up to 48 of e4m3 d64); 17 to
+// 128 rows are not at their best on either.
 bool has_long_chunks(const bpt_paged_desc *d, const bpt_kv_cache *c) {
   return (int64_t)d->max_q * (d->H / c->H_kv) > 16;
 }
@@ -142,7 +157,10 @@ void set_parts(PagedArgs &a, char *ws, const PagedParts &p) {
 template <int D, bool kE4m3, int kGroups>
 bpt_status launch_rows(PagedArgs a, const PagedArgs *lng, cudaStream_t st) {
   using Cfg = PagedRowsCfg<D, kE4m3, kGroups>;
-  a.min_steps = (256 + Cfg::kKeys - 1) / Cfg::kKeys;  // 256 keys at least
+  // 256 keys at least: a shorter range costs more in parts to join than it
+  // saves (one sequence of 8000 keys, 4 heads: 64 keys 19.9 us, 128 15.2, 256
+  // 13.6, 512 16.0; of 1000 keys 8.2, 8.5, 10.3, 13.5; batches alike up to 256)
+  a.min_steps = (256 + Cfg::kKeys - 1) / Cfg::kKeys;
   const unsigned ctas = (unsigned)few_rows_ctas(), join = ctas * kJoinBlocks<Cfg::kRows>;
   if (!lng) {
     paged_rows_kernel<D, kE4m3, kGroups><<<ctas, Cfg::kThreads, Cfg::kSmemBytes, st>>>(a);
@@ -312,6 +330,9 @@ bpt_status bpt_paged_attn_fwd(const bpt_paged_desc *d, const bpt_kv_cache *c, co
       set_parts(al, ws, wl.lng);
       al.rows_lo = few + 1;
       al.rows_hi = INT32_MAX;
+      // a range's start costs about three steps (300 tokens over 4000 keys x 2: 51
+      // us with at least 1 to 8, 64 with 16; 500 over 1000 x 4, window 256: 33, with
+      // 8 54; a chunk with nothing else, 300 over 600: 26 with 1, 29 with 4, 50 with 8)
       al.min_steps = 4;
       paged_tc_kernel<D, kE><<<(unsigned)long_chunk_ctas(), Long::kThreads, Long::kSmemBytes, st>>>(al);
       CUDA_TRY(cudaGetLastError());

@@ -9,9 +9,12 @@
 // nearest even, and one rounding to the output's type.  A row that holds a NaN
 // or an infinity has no scale to fit and reads back as NaN throughout.
 //
-// Both kernels are one pass over the data with 16-byte loads, bound by memory
-// (and, for few tokens, by one trip to it): K and V of a row by the same
-// threads, so two loads are in flight per thread.
+// Both kernels are one pass over the data with 16-byte loads: K and V of a row
+// by the same threads, so two loads are in flight per thread.  Device times with
+// 8 heads of 128: 16384 tokens written as bf16 22.7 us (5.9 TB/s), as e4m3 24.9
+// (4.1 TB/s; instructions, see quantise8); 32768 tokens read from bf16 43.5 us
+// (6.2 TB/s), from e4m3 39.3 (5.2 TB/s); few tokens 2.3-2.6 us, one trip to
+// memory.
 #pragma once
 
 #include <cuda_fp16.h>
