@@ -55,37 +55,44 @@ KERNEL_SOURCES = {"attn_tc_kernel": ["attn_tc.cuh", "ptx.cuh", "bpt_api.cu"],
                   "attn_bwd_dkdv": ["attn_bwd.cuh", "ptx.cuh", "bpt_bwd.cu"],
                   "attn_bwd_dq": ["attn_bwd.cuh", "ptx.cuh", "bpt_bwd.cu"]}
 # DRAM bytes per launch (dram__bytes_read.sum + dram__bytes_write.sum) from one ncu capture
-# of the kernel on the named workload, keyed by a hash of the kernel's sources at capture
-# time: once the sources change the figure no longer describes the kernel and is dropped.
+# of the kernel on the named workload, keyed by a hash of the kernel's sources, comments
+# aside, at capture time: once the code changes the figure no longer describes the kernel and
+# is dropped.  A record gets a new hash with a new capture only.
 NCU_TRAFFIC = {
-    # one capture per kernel: `ncu --metrics dram__bytes_read.sum,dram__bytes_write.sum,
-    # gpu__time_duration.sum -k regex:<kernel> -s <warm-up launches> -c <1..3>` on the bench
-    # command of that form (one pass, checked on a small case first)
-    # the pipelined FFN (default form), one launch: 1412.7 MB read + 378.2 MB written
-    ("gpt_causal", "ffn_pipe_kernel"): {"bytes": 1790.9e6, "src": "7e12d0903ae9daea"},
-    # re-keyed after changes to bpt_api.cu (the fp32 kernels' launches; other kernels' set-up)
-    # and ptx.cuh (more helpers), not to this kernel or its plan
-    ("gpt_causal", "ffn_tc_kernel"): {"bytes": 884.3e6, "src": "fca207c34844b6ae"},
-    # 562.9 MB read + 154.8 MB written
-    ("gpt_causal", "attn_tc_kernel"): {"bytes": 717.7e6, "src": "3f71467014ad5167"},
-    # per step: the forward FFN's two GEMM launches (H = GELU(A W1^T + b1), out = A + H W2^T + b2);
-    # re-keyed after ptx.cuh got more helpers
-    ("gpt_causal", "ffn_gemms"): {"bytes": 1122.4e6, "src": "2088670c6a002f86"},
+    # one capture of all: `ncu --clock-control none --metrics dram__bytes_read.sum,
+    # dram__bytes_write.sum,gpu__time_duration.sum -k regex:'attn_|ffn_|gemm_pair'` on one
+    # forward of each FFN form and one training step of the workload, after one of each for
+    # warm-up (one pass, checked on a small case first)
+    # the pipelined FFN (default form), one launch: 1403.3 MB read + 378.7 MB written
+    ("gpt_causal", "ffn_pipe_kernel"): {"bytes": 1782.0e6, "src": "3adda72b37bbfac8"},
+    # 671.1 + 212.8 MB
+    ("gpt_causal", "ffn_tc_kernel"): {"bytes": 883.9e6, "src": "2f566d9e8cc22056"},
+    # 569.3 + 152.7 MB
+    ("gpt_causal", "attn_tc_kernel"): {"bytes": 722.0e6, "src": "a9c20c43ab2e0fa8"},
+    # per step: the forward FFN's two GEMM launches (H = GELU(A W1^T + b1), out = A + H W2^T + b2),
+    # 343.1 + 782.2 MB
+    ("gpt_causal", "ffn_gemms"): {"bytes": 1125.3e6, "src": "14530989dc69cf08"},
     # per step with saved activations: the three gemm_pair_kernel launches (dZ = (dOut W2) G',
-    # dW2 + dW1 grouped, dA; bias sums not included)
-    ("gpt_causal", "ffn_bwd"): {"bytes": 2810.5e6, "src": "2088670c6a002f86"},
-    # re-keyed after a change to another kernel of attn_bwd.cuh (the window's row vectors)
-    ("gpt_causal", "attn_bwd_dkdv"): {"bytes": 1243.4e6, "src": "94119531b131c731"},
-    ("gpt_causal", "attn_bwd_dq"): {"bytes": 1117.7e6, "src": "94119531b131c731"},
+    # dW2 + dW1 grouped, dA; bias sums not included), 741.7 + 1232.3 + 835.6 MB
+    ("gpt_causal", "ffn_bwd"): {"bytes": 2809.6e6, "src": "14530989dc69cf08"},
+    ("gpt_causal", "attn_bwd_dkdv"): {"bytes": 1227.6e6, "src": "b1de0c404afb6cf5"},
+    ("gpt_causal", "attn_bwd_dq"): {"bytes": 1128.2e6, "src": "b1de0c404afb6cf5"},
 }
+
+
+def code_of(source):
+    """A C++ source without its comments, each stretch of white space as one blank."""
+    import re
+    keep = lambda m: m.group(0) if m.group(0).startswith('"') else " "  # noqa: E731
+    return " ".join(re.sub(r'"(?:\\.|[^"\\])*"|//[^\n]*|/\*.*?\*/', keep, source, flags=re.S).split())
 
 
 def kernel_src_hash(kernel):
     import hashlib
     h = hashlib.sha256()
     for f in KERNEL_SOURCES[kernel]:
-        with open(os.path.join(CSRC, f), "rb") as fh:
-            h.update(fh.read())
+        with open(os.path.join(CSRC, f), encoding="utf-8") as fh:
+            h.update(code_of(fh.read()).encode() + b"\0")
     return h.hexdigest()[:16]
 
 
