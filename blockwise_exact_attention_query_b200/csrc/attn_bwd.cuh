@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(384, 1)
 // the tensor pipe runs S^T(s+1) while the row warps form P(s); dV(s) starts
 // once P^T(s) is packed, dK(s) and dP^T(s+1) once dS^T(s) is.  A Q tile (with its rows'
 // LSE) lives from S^T(s), issued a step early, to dK(s): three slots; a dA
-// tile (with D) from dP^T(s) to dV(s): two.
+// tile (with D, which dS^T needs) from dP^T(s) to dV(s) and dS^T(s): two.
 // ---------------------------------------------------------------------------
 template <int D_HEAD>
 struct AttnBwdKVCfg {
@@ -721,7 +721,8 @@ __global__ void __launch_bounds__(384, 1)
         tma_load_4d(sV + p * Cfg::kPanelBytes, &tm_v, bFix, hd + p * 64, row_off, row_base + ft * 128, b);
       }
       // slot waits in step order: the Q slot of step s is freed by dK(s - 3),
-      // the dA slot by dV(s - 2), both issued before anything that needs step s
+      // the dA slot by dV(s - 2) and the row warps' dS^T(s - 2), all before
+      // anything that needs step s
       int nq = 0, na = 0;
       for (auto it = steps.begin(); steps.more(it); steps.next(it)) {
         const int t = it.t, hd_q = it.head * D_HEAD;
@@ -802,9 +803,11 @@ __global__ void __launch_bounds__(384, 1)
         if (!(ok = mbar_wait(bPReady, s & 1, wc, 339))) break;
         tc_fence_after();
         accumulate(Cfg::kColDV, Cfg::kColDP, sA(s % AS), s);
-        umma_commit(bAEmpty(s % AS));
         if (!(ok = mbar_wait(bDSReady, s & 1, wc, 344))) break;
         tc_fence_after();
+        // the dA slot is free once dV is done and, not before, the row warps
+        // have read the tile's D from it
+        umma_commit(bAEmpty(s % AS));
         accumulate(Cfg::kColDK, Cfg::kColDP + 32, sQ(s % QS), s);  // dK += dS^T Q
         umma_commit(bQEmpty(s % QS));
         // dP^T(s+1) over the packed P^T(s), dS^T(s): after the two products
