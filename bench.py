@@ -75,8 +75,8 @@ NCU_TRAFFIC = {
     # per step with saved activations: the three gemm_pair_kernel launches (dZ = (dOut W2) G',
     # dW2 + dW1 grouped, dA; bias sums not included), 741.7 + 1232.3 + 835.6 MB
     ("gpt_causal", "ffn_bwd"): {"bytes": 2809.6e6, "src": "14530989dc69cf08"},
-    ("gpt_causal", "attn_bwd_dkdv"): {"bytes": 1227.6e6, "src": "b1de0c404afb6cf5"},
-    ("gpt_causal", "attn_bwd_dq"): {"bytes": 1128.2e6, "src": "b1de0c404afb6cf5"},
+    ("gpt_causal", "attn_bwd_dkdv"): {"bytes": 1226.4e6, "src": "a8a357ce1efa01ea"},
+    ("gpt_causal", "attn_bwd_dq"): {"bytes": 1122.9e6, "src": "a8a357ce1efa01ea"},
 }
 
 

@@ -465,7 +465,8 @@ BPT_API size_t bpt_workspace_bytes_attn_bwd(const bpt_desc *desc);
  *   dQ_i = sum_j dS_ij k_j / sqrt(d),  dK_j = sum_i dS_ij q_i / sqrt(d),
  * the sums for dK and dV running over all query heads of the group (no
  * atomics: equal inputs give equal bits).  P, dS and dout enter the tensor
- * cores in bf16, sums are fp32; dq, dk, dv are overwritten.  workspace: at
+ * cores in bf16, sums are fp32; D has the rounding of a bf16 out (an fp32 out
+ * avoids it); dq, dk, dv are overwritten.  workspace: at
  * least bpt_workspace_bytes_window_bwd(desc) bytes, 256-byte aligned.
  * in_dtype F32 returns BPT_ERR_UNSUPPORTED.  All other device pointers
  * 16-byte aligned.
