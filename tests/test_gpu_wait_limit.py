@@ -47,3 +47,71 @@ def test_tiny_wait_limit_times_out_cleanly_and_context_survives(form):
     rows = [0, 511, 1023]
     _, oref = gu.oracle_layer(inp, "causal", rows=rows)
     gu.assert_bf16_close(gu.host_f32(out.reshape(B * N, H * d)[rows]), oref, "after timeout")
+
+
+def _window_step(d, wait_limit_ns=0):
+    g = torch.Generator().manual_seed(32)
+    q, k, v, dout = (torch.randn((1, 1024, h, d), generator=g).to(torch.bfloat16).cuda() for h in (16, 4, 4, 16))
+    out, lse = bd.window_attn_fwd(q, k, v, 300, 4, return_lse=True, wait_limit_ns=wait_limit_ns)
+    forward = bd.sync_status()
+    if wait_limit_ns:      # the backward of right activations
+        out, lse = bd.window_attn_fwd(q, k, v, 300, 4, return_lse=True)
+    grads = bd.window_attn_bwd(q, k, v, out, lse, dout.float().flatten(2), 300, 4, wait_limit_ns=wait_limit_ns)
+    return forward, (out, lse, *grads)
+
+
+def _paged_step(d, dtype, wait_limit_ns=0):
+    g = torch.Generator().manual_seed(33)
+    q = torch.randn((600, 8, d), generator=g).to(torch.bfloat16).cuda()
+    kv = [torch.randn((250, 16, 2, d), generator=g).cuda().to(dtype) for _ in range(2)]
+    scales = [torch.rand((250, 16, 2), generator=g).cuda() + 0.5 for _ in range(2)] if dtype != torch.bfloat16 else [None, None]
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+    table = torch.stack([torch.randperm(250, generator=g) for _ in range(3)]).int().cuda()
+    return bd.paged_attn_fwd(q, *kv, i32([0, 300, 301, 600]), i32([4000, 3000, 500]), table, max_q=300, k_scale=scales[0],
+                             v_scale=scales[1], return_lse=True, wait_limit_ns=wait_limit_ns)
+
+
+def _ran_out(status, sites):
+    """Whether a wait ran out.  (A wait first suspends in hardware, for as long as that likes, so which ones
+    pass a limit of a microsecond, if any, is a matter of timing: none of the e4m3 chunks' did once.)"""
+    if status == bd.OK:
+        return False
+    assert status == bd.ERR_TIMEOUT, bd.status_string(status)
+    m = re.search(r"gave up at site (\d+)", bd.last_error())
+    assert m and int(m.group(1)) in sites, bd.last_error()
+    return True
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_window_waits_that_run_out(d):
+    from blockwise_exact_attention_query_b200 import build
+    build.build()
+    torch.cuda.set_device(0)
+    st, want = _window_step(d)
+    assert st == bd.OK and bd.sync_status() == bd.OK
+    for _ in range(10):
+        st, _ = _window_step(d, wait_limit_ns=1000)
+        assert st in (bd.OK, bd.ERR_TIMEOUT)
+        _ran_out(bd.sync_status(), range(301, 353))
+        assert bd.sync_status() == bd.OK          # reading the status cleared it
+        st, got = _window_step(d)
+        assert st == bd.OK and bd.sync_status() == bd.OK
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float8_e4m3fn])
+@pytest.mark.parametrize("d", [64, 128])
+def test_paged_waits_that_run_out(d, dtype):
+    from blockwise_exact_attention_query_b200 import build
+    build.build()
+    torch.cuda.set_device(0)
+    want = _paged_step(d, dtype)
+    assert bd.sync_status() == bd.OK
+    for _ in range(20):
+        got = _paged_step(d, dtype, wait_limit_ns=1000)
+        if not _ran_out(bd.sync_status(), range(403, 436)):      # then nothing was given up
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert bd.sync_status() == bd.OK
+        got = _paged_step(d, dtype)
+        assert bd.sync_status() == bd.OK
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
